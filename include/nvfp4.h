@@ -250,6 +250,118 @@ nvfp4_status nvfp4_gemm_ex3(const uint8_t* A, const uint8_t* sfA, const uint8_t*
                             nvfp4_sf_layout sf_layout, nvfp4_out_dtype out_dtype, uint32_t flags,
                             cudaStream_t stream);
 
+/* Activation functions of the fused products, evaluated in fp32. */
+typedef enum {
+    NVFP4_ACT_NONE = 0,
+    NVFP4_ACT_RELU = 1,       /* max(v, 0) */
+    NVFP4_ACT_GELU = 2,       /* v Phi(v) = v / 2 (1 + erf(v / sqrt 2)) */
+    NVFP4_ACT_GELU_TANH = 3,  /* v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) */
+    NVFP4_ACT_SILU = 4,       /* v / (1 + exp(-v)) */
+    NVFP4_ACT_RELU2 = 5       /* max(v, 0)^2 */
+} nvfp4_act;
+
+/*
+ * nvfp4_gemm with bias, activation and residual in its epilogue (the pages' product has none of
+ * them: they are what a transformer block puts around it):
+ *     out[m, n] = act(alpha[0] * sum_k deq(A)[m, k] deq(B)[n, k] + bias[n])
+ *                 + residual_scale * residual[m, n]
+ * computed in fp32 and rounded once to out_dtype. sfA, sfB: NVFP4_SF_TILED. bias[N]: fp32
+ * (device), or NULL for none. residual[M, N]: out_dtype elements, row-major (device), or NULL for
+ * none; it may be out itself (each element is read before its place is written), but no other
+ * array that overlaps out. residual_scale is a host value, not used without residual. flags:
+ * NVFP4_GEMM_B_READY as for nvfp4_gemm_ex3. No workspace: split-K reduces inside a thread-block
+ * cluster, in a fixed order. Shapes and alignment as for nvfp4_gemm; bias and residual 16-byte
+ * aligned. A bad act, out_dtype or flag: NVFP4_ERR_INVALID_ARG.
+ */
+nvfp4_status nvfp4_gemm_epilogue(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                                 const float* alpha, void* out, int64_t M, int64_t N, int64_t K,
+                                 const float* bias, nvfp4_act act, const void* residual, float residual_scale,
+                                 nvfp4_out_dtype out_dtype, uint32_t flags, cudaStream_t stream);
+
+/*
+ * Re-lays the row-major scales sf[2 I][K/16] (device) of a gate_up weight (gate rows [0, I), then up
+ * rows [I, 2 I)) out for the gated products below, into out (device, nvfp4_sf_bytes(2 I, K,
+ * NVFP4_SF_TILED) bytes; padding rows become 0): the tiled layout of the rows taken in groups of
+ * 16 gate rows and the 16 up rows of the same index, i.e. row 32 t + i of that order is gate row
+ * 16 t + i, row 32 t + 16 + i up row I + 16 t + i (i < 16). I % 16 == 0, K % 64 == 0. For weights,
+ * once. The codes stay as they are.
+ */
+nvfp4_status nvfp4_gate_up_sf_tile(const uint8_t* sf, int64_t I, int64_t K, uint8_t* out, cudaStream_t stream);
+
+/*
+ * The first half of a gated feed-forward block in one kernel: both projections, the activation and
+ * the product. With v = alpha[0] * deq(A) deq(B)^T in fp32 ([M, 2 I], never stored),
+ *     g = v[m, j],  u = v[m, I + j],  h[m, j] = act(g) * u        (j < I)
+ * A[M, K/2] with sfA NVFP4_SF_TILED; B[2 I, K/2] holds the gate rows [0, I) then the up rows, as for
+ * nvfp4_grouped_gemm_swiglu (whose dense counterpart this is), sfB its scales from
+ * nvfp4_gate_up_sf_tile. act = NVFP4_ACT_SILU is SwiGLU, NVFP4_ACT_GELU GeGLU, and so on.
+ *   nvfp4_gemm_glu:          h[M, I] in out_dtype, rounded once.
+ *   nvfp4_gemm_glu_quantize: h quantised as nvfp4_quantize does with the fixed global scale gs_h
+ *                            (device, one float): h_q[M, I/2], and h_sf in h_sf_layout
+ *                            (NVFP4_SF_LINEAR or NVFP4_SF_TILED, nvfp4_sf_bytes(M, I, layout)
+ *                            bytes, padding left as it is): the A operand of the down projection.
+ *   nvfp4_gemm_glu_backward: the gradients of g and u from dh[M, I], with g and u computed again
+ *                            by the same product (the forward call stores neither):
+ *                                dgu[m, j] = dh * u * act'(g),  dgu[m, I + j] = dh * act(g)
+ *                            dh and dgu[M, 2 I] in dtype, dgu rounded once; they must not overlap.
+ *                            act' is 0 at the kink of relu. The gradient of the block's input is
+ *                            then nvfp4_gemm of the quantised dgu with the transposed weights.
+ * I % 32 == 0 (NVFP4_SF_TILED h_sf: I % 64 == 0), otherwise shapes, alignment, flags and determinism
+ * as for nvfp4_gemm_epilogue; h, h_q, h_sf, dh, dgu 16-byte aligned, gs_h 4-byte aligned.
+ */
+nvfp4_status nvfp4_gemm_glu(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                            const float* alpha, void* h, int64_t M, int64_t I, int64_t K, nvfp4_act act,
+                            nvfp4_out_dtype out_dtype, uint32_t flags, cudaStream_t stream);
+
+nvfp4_status nvfp4_gemm_glu_quantize(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                                     const float* alpha, int64_t M, int64_t I, int64_t K, nvfp4_act act,
+                                     const float* gs_h, uint8_t* h_q, uint8_t* h_sf, nvfp4_sf_layout h_sf_layout,
+                                     uint32_t flags, cudaStream_t stream);
+
+nvfp4_status nvfp4_gemm_glu_backward(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                                     const float* alpha, const void* dh, void* dgu, int64_t M, int64_t I, int64_t K,
+                                     nvfp4_act act, nvfp4_out_dtype dtype, uint32_t flags, cudaStream_t stream);
+
+/* Norms of nvfp4_residual_norm, over the H elements of a row. */
+typedef enum {
+    NVFP4_NORM_RMS = 0,     /* N(z) = z / sqrt(mean(z^2) + eps) */
+    NVFP4_NORM_LAYER = 1    /* N(z) = (z - mean(z)) / sqrt(mean((z - mean(z))^2) + eps) */
+} nvfp4_norm;
+
+/*
+ * The residual add and the norms around a transformer block, one pass: per row of x and y [rows, H],
+ *     v = y;   v = N(v) * post_weight;   v = gate * v         (the last two where given)
+ *     r = x + residual_scale * v, rounded to dtype            (r = x where y is NULL)
+ *     n = N(r) * weight + bias                                (bias where given)
+ * in fp32; the norm is of r as it is stored. x is the residual stream, y the output of the block
+ * before (NULL: none; then post_weight, gate and r_out must be NULL too), post_weight the norm
+ * behind that block, gate[H] its channel gate, weight the norm before the next block.
+ *   nvfp4_residual_norm:          out[rows, H] = n in out_dtype, rounded once.
+ *   nvfp4_residual_norm_quantize: n quantised as nvfp4_quantize does with the fixed global scale gs
+ *                                 (device, one float): q[rows, H/2] and sf in sf_layout
+ *                                 (NVFP4_SF_LINEAR or NVFP4_SF_TILED, nvfp4_sf_bytes(rows, H,
+ *                                 layout) bytes, padding left as it is): the A operand of the
+ *                                 products that read the block's input.
+ * x, y, r_out: dtype elements, rows ld_x, ld_y, ld_r elements apart (each >= H, a multiple of 16
+ * bytes). r_out may be NULL (r is not stored), x or y themselves (with the same row stride), but
+ * overlap nothing else; out, q and sf overlap no input. weight, bias, post_weight, gate: fp32 [H].
+ * H % 8 == 0 (quantised: H % 16, NVFP4_SF_TILED: H % 64), H <= 32768; every pointer 16-byte aligned
+ * (gs: 4). residual_scale and eps >= 0 are host values. rows == 0 or H == 0 is a no-op. One launch;
+ * sums are fp32 in a fixed order (deterministic).
+ */
+nvfp4_status nvfp4_residual_norm(const void* x, const void* y, nvfp4_out_dtype dtype, int64_t rows, int64_t H,
+                                 int64_t ld_x, int64_t ld_y, nvfp4_norm norm, const float* weight, const float* bias,
+                                 const float* post_weight, const float* gate, float residual_scale, float eps,
+                                 void* r_out, int64_t ld_r, void* out, nvfp4_out_dtype out_dtype,
+                                 cudaStream_t stream);
+
+nvfp4_status nvfp4_residual_norm_quantize(const void* x, const void* y, nvfp4_out_dtype dtype, int64_t rows,
+                                          int64_t H, int64_t ld_x, int64_t ld_y, nvfp4_norm norm,
+                                          const float* weight, const float* bias, const float* post_weight,
+                                          const float* gate, float residual_scale, float eps, void* r_out,
+                                          int64_t ld_r, const float* gs, uint8_t* q, uint8_t* sf,
+                                          nvfp4_sf_layout sf_layout, cudaStream_t stream);
+
 /*
  * MXFP4: the mm_fp4 variant that use_nvfp4=False selects ("The Art of Reading the Manual",
  * section "The Message"; the pages name it without defining it). The library's reading is

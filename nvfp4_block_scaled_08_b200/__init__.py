@@ -29,7 +29,8 @@ from . import _build
 
 __all__ = [
     "Nvfp4Error", "load", "global_scale", "quantize", "quantize_dynamic", "alpha", "gemm", "gemm_workspace_size",
-    "gemm_noalloc", "gemm_act", "plan_override",
+    "gemm_noalloc", "gemm_act", "plan_override", "gemm_epilogue", "gate_up_sf_tile", "gemm_glu",
+    "gemm_glu_quantize", "gemm_glu_backward", "residual_norm", "residual_norm_quantize",
     "make_workspace", "grouped_gemm", "grouped_gemm_swiglu", "moe_route", "moe_gather_quantize",
     "moe_combine", "mx_quantize", "mx_sf_tile", "mx_sf_bytes", "mx_gemm", "round_e4m3", "round_e2m1", "last_device_error",
     "STATUS",
@@ -53,7 +54,7 @@ _lib = None
 _lock = threading.Lock()
 
 # exported symbol -> (restype, argtypes)
-_P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_P, _I64, _I32, _SZ, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "nvfp4_global_scale": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _P]),
@@ -89,6 +90,19 @@ SIGNATURES = {
     "nvfp4_mx_gemm": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, ctypes.c_int, _P]),
     "nvfp4_gemm_act": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P,
                                       ctypes.c_int, _P]),
+    "nvfp4_gemm_epilogue": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_int, _P, _F,
+                                           ctypes.c_int, ctypes.c_uint32, _P]),
+    "nvfp4_gate_up_sf_tile": (ctypes.c_int, [_P, _I64, _I64, _P, _P]),
+    "nvfp4_gemm_glu": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int,
+                                      ctypes.c_uint32, _P]),
+    "nvfp4_gemm_glu_quantize": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, _P, _P, _P,
+                                               ctypes.c_int, ctypes.c_uint32, _P]),
+    "nvfp4_gemm_glu_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int,
+                                               ctypes.c_int, ctypes.c_uint32, _P]),
+    "nvfp4_residual_norm": (ctypes.c_int, [_P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, ctypes.c_int, _P, _P, _P,
+                                           _P, _F, _F, _P, _I64, _P, ctypes.c_int, _P]),
+    "nvfp4_residual_norm_quantize": (ctypes.c_int, [_P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, ctypes.c_int, _P,
+                                                    _P, _P, _P, _F, _F, _P, _I64, _P, _P, _P, ctypes.c_int, _P]),
     "nvfp4_grouped_gemm_workspace_size": (_SZ, [_I32, _I64, _I64, _I64]),
     "nvfp4_grouped_gemm": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _P, _P,
                                           _SZ, _P]),
@@ -385,6 +399,199 @@ def grouped_gemm_swiglu(Aq, sfA, Bq, sfB, alphas, offsets, gs_h, h_q=None, h_sf=
         _ptr(Aq), _ptr(sfA), _ptr(Bq), _ptr(sfB), _ptr(alphas), _ptr(offsets), E, rows, I, K,
         _ptr(gs_h), _ptr(h_q), _ptr(h_sf), _stream(stream)))
     return h_q, h_sf
+
+
+# ------------------------------------------------------------------ fused products and norms
+
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "relu2": 5}
+NORMS = {"rms": 0, "layer": 1}
+
+
+def _code(table: dict, name: str, what: str) -> int:
+    if name not in table:
+        raise ValueError(f"{what} must be one of {', '.join(table)}")
+    return table[name]
+
+
+def _arg(t, name: str, dtype, shape=None, numel=None, device=None) -> int | None:
+    """The address of a contiguous CUDA tensor of this type and shape (or with at least `numel`
+    elements) on `device`; None for None. The kernels trust sizes, so the binding checks them."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if numel is not None and t.numel() < numel:
+        raise ValueError(f"{name} needs at least {numel} elements")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.data_ptr()
+
+
+def _on_current_device(t: torch.Tensor, name: str):
+    _dev(t, name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return t.device
+
+
+def _tiled_bytes(rows: int, K: int) -> int:
+    return (rows + 127) // 128 * 128 * (K // 16)
+
+
+def _operands(Aq, sfA, Bq, sfB, alpha_t):
+    """Checked addresses of A and B with tiled scales and alpha, and (M, N, K, device)."""
+    dev = _on_current_device(Aq, "Aq")
+    if Aq.dim() != 2 or Bq.dim() != 2 or Aq.shape[1] != Bq.shape[1]:
+        raise ValueError("Aq and Bq must be [rows, K/2] with the same K")
+    (M, k2), N = Aq.shape, Bq.shape[0]
+    u8, K = torch.uint8, 2 * k2
+    return (_arg(Aq, "Aq", u8), _arg(sfA, "sfA", u8, numel=_tiled_bytes(M, K), device=dev),
+            _arg(Bq, "Bq", u8, device=dev), _arg(sfB, "sfB", u8, numel=_tiled_bytes(N, K), device=dev),
+            _arg(alpha_t, "alpha", torch.float32, numel=1, device=dev)), M, N, K, dev
+
+
+def gemm_epilogue(Aq, sfA, Bq, sfB, alpha_t, out=None, *, bias=None, act: str = "none", residual=None,
+                  residual_scale: float = 1.0, out_dtype=torch.bfloat16, b_ready: bool = False,
+                  stream=None) -> torch.Tensor:
+    """out[M, N] = act(alpha * deq(A) deq(B)^T + bias) + residual_scale * residual, one kernel.
+
+    Operands as for gemm(tiled=True); bias fp32 [N]; act one of ACTS; residual [M, N] of out's
+    dtype, which may be out itself; b_ready as for gemm."""
+    ops, M, N, K, dev = _operands(Aq, sfA, Bq, sfB, alpha_t)
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    _check("nvfp4_gemm_epilogue", load().nvfp4_gemm_epilogue(
+        *ops, _arg(out, "out", out.dtype, (M, N), device=dev), M, N, K,
+        _arg(bias, "bias", torch.float32, (N,), device=dev), _code(ACTS, act, "act"),
+        _arg(residual, "residual", out.dtype, (M, N), device=dev), residual_scale, _out_code(out),
+        1 if b_ready else 0, _stream(stream)))
+    return out
+
+
+def gate_up_sf_tile(sf: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Row-major scales [2I, K/16] of a gate_up weight (gate rows, then up rows) -> the scales
+    that gemm_glu and its relatives take (flat uint8 tensor); once per weight."""
+    dev = _on_current_device(sf, "sf")
+    if sf.dim() != 2 or sf.shape[0] % 2:
+        raise ValueError("sf must be [2I, K/16]")
+    rows, K = sf.shape[0], sf.shape[1] * 16
+    if out is None:
+        out = torch.empty(_tiled_bytes(rows, K), dtype=torch.uint8, device=dev)
+    _check("nvfp4_gate_up_sf_tile", load().nvfp4_gate_up_sf_tile(
+        _arg(sf, "sf", torch.uint8), rows // 2, K,
+        _arg(out, "out", torch.uint8, numel=_tiled_bytes(rows, K), device=dev), _stream(stream)))
+    return out
+
+
+def _glu_operands(Aq, sfA, Bq, sfB, alpha_t):
+    ops, M, N, K, dev = _operands(Aq, sfA, Bq, sfB, alpha_t)
+    if N % 2:
+        raise ValueError("Bq must hold as many up rows as gate rows")
+    return ops, M, N // 2, K, dev
+
+
+def gemm_glu(Aq, sfA, Bq, sfB, alpha_t, out=None, *, act: str = "silu", out_dtype=torch.bfloat16,
+             b_ready: bool = False, stream=None) -> torch.Tensor:
+    """Gated feed-forward product h[M, I] = act(g) * u, [g | u] = alpha * deq(A) deq(B)^T, one kernel.
+
+    Aq [M, K/2] with tiled scales; Bq [2I, K/2] gate rows then up rows, sfB from gate_up_sf_tile."""
+    ops, M, I, K, dev = _glu_operands(Aq, sfA, Bq, sfB, alpha_t)
+    if out is None:
+        out = torch.empty(M, I, dtype=out_dtype, device=dev)
+    _check("nvfp4_gemm_glu", load().nvfp4_gemm_glu(
+        *ops, _arg(out, "out", out.dtype, (M, I), device=dev), M, I, K, _code(ACTS, act, "act"),
+        _out_code(out), 1 if b_ready else 0, _stream(stream)))
+    return out
+
+
+def gemm_glu_quantize(Aq, sfA, Bq, sfB, alpha_t, gs_h, h_q=None, h_sf=None, *, act: str = "silu",
+                      tiled: bool = True, b_ready: bool = False, stream=None):
+    """gemm_glu with h quantised to NVFP4 under the fixed global scale gs_h (fp32 [1], device).
+
+    Returns (h_q uint8 [M, I/2], h_sf: flat tiled scales, or [M, I/16] if not tiled)."""
+    ops, M, I, K, dev = _glu_operands(Aq, sfA, Bq, sfB, alpha_t)
+    if h_q is None:
+        h_q = torch.empty(M, I // 2, dtype=torch.uint8, device=dev)
+    n = _tiled_bytes(M, I) if tiled else M * (I // 16)
+    if h_sf is None:
+        h_sf = torch.empty(n, dtype=torch.uint8, device=dev)
+        h_sf = h_sf if tiled else h_sf.view(M, I // 16)
+    _check("nvfp4_gemm_glu_quantize", load().nvfp4_gemm_glu_quantize(
+        *ops, M, I, K, _code(ACTS, act, "act"), _arg(gs_h, "gs_h", torch.float32, numel=1, device=dev),
+        _arg(h_q, "h_q", torch.uint8, (M, I // 2), device=dev),
+        _arg(h_sf, "h_sf", torch.uint8, numel=n, device=dev), SF_TILED if tiled else SF_LINEAR,
+        1 if b_ready else 0, _stream(stream)))
+    return h_q, h_sf
+
+
+def gemm_glu_backward(Aq, sfA, Bq, sfB, alpha_t, dh, out=None, *, act: str = "silu", b_ready: bool = False,
+                      stream=None) -> torch.Tensor:
+    """Gradients of gemm_glu's g and u from dh [M, I]: [M, 2I] = [dh * u * act'(g) | dh * act(g)] in
+    dh's dtype, with g and u computed again by the same product (one kernel)."""
+    ops, M, I, K, dev = _glu_operands(Aq, sfA, Bq, sfB, alpha_t)
+    if out is None:
+        out = torch.empty(M, 2 * I, dtype=dh.dtype, device=dev)
+    _check("nvfp4_gemm_glu_backward", load().nvfp4_gemm_glu_backward(
+        *ops, _arg(dh, "dh", out.dtype, (M, I), device=dev),
+        _arg(out, "out", out.dtype, (M, 2 * I), device=dev), M, I, K, _code(ACTS, act, "act"),
+        _out_code(out), 1 if b_ready else 0, _stream(stream)))
+    return out
+
+
+def _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out):
+    """The leading arguments of both residual norms, and r (allocated where y asks for it)."""
+    dev = _on_current_device(x, "x")
+    if x.dim() != 2 or x.dtype not in OUT_DTYPES:
+        raise ValueError("x must be [rows, H] in bfloat16, float16 or float32")
+    rows, H = x.shape
+    if y is not None and r_out is None:
+        r_out = torch.empty(rows, H, dtype=x.dtype, device=dev)
+    for t, name in ((x, "x"), (y, "y"), (r_out, "r_out")):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != dev or (H > 1 and t.stride(1) != 1)):
+            raise ValueError(f"{name} must be like x, with unit column stride")
+    f32 = torch.float32
+    vec = [_arg(t, name, f32, (H,), device=dev) for t, name in
+           ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (gate, "gate"))]
+    ld = [0 if t is None else t.stride(0) if rows > 1 else H for t in (x, y, r_out)]
+    args = (x.data_ptr(), _ptr(y), OUT_DTYPES[x.dtype], rows, H, ld[0], ld[1], _code(NORMS, kind, "kind"), *vec,
+            residual_scale, eps, _ptr(r_out), ld[2])
+    return args, (x if y is None else r_out), rows, H, dev
+
+
+def residual_norm(x, weight, y=None, *, kind: str = "rms", bias=None, post_weight=None, gate=None,
+                  residual_scale: float = 1.0, eps: float = 1e-6, r_out=None, out=None, out_dtype=None, stream=None):
+    """Residual add and norms around a block, one pass: r = x + residual_scale * v with v = y, its
+    own norm times post_weight (if given) and gate * v (if given); out = N(r) * weight + bias.
+
+    x, y [rows, H] (bf16, fp16 or fp32, unit column stride); weight, bias, post_weight, gate fp32
+    [H]; r_out may be x or y (the residual updated in place). Returns (out, r); r is x without y."""
+    args, r, rows, H, dev = _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out)
+    if out is None:
+        out = torch.empty(rows, H, dtype=out_dtype or x.dtype, device=dev)
+    _check("nvfp4_residual_norm", load().nvfp4_residual_norm(
+        *args, _arg(out, "out", out.dtype, (rows, H), device=dev), _out_code(out), _stream(stream)))
+    return out, r
+
+
+def residual_norm_quantize(x, weight, gs, y=None, *, kind: str = "rms", bias=None, post_weight=None, gate=None,
+                           residual_scale: float = 1.0, eps: float = 1e-6, r_out=None, q=None, sf=None,
+                           tiled: bool = True, stream=None):
+    """residual_norm with the normed rows quantised to NVFP4 under the fixed global scale gs (fp32
+    [1], device). Returns (q uint8 [rows, H/2], sf: flat tiled scales, or [rows, H/16] if not
+    tiled, r)."""
+    args, r, rows, H, dev = _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out)
+    if q is None:
+        q = torch.empty(rows, H // 2, dtype=torch.uint8, device=dev)
+    n = _tiled_bytes(rows, H) if tiled else rows * (H // 16)
+    if sf is None:
+        sf = torch.empty(n, dtype=torch.uint8, device=dev)
+        sf = sf if tiled else sf.view(rows, H // 16)
+    _check("nvfp4_residual_norm_quantize", load().nvfp4_residual_norm_quantize(
+        *args, _arg(gs, "gs", torch.float32, numel=1, device=dev), _arg(q, "q", torch.uint8, (rows, H // 2), device=dev),
+        _arg(sf, "sf", torch.uint8, numel=n, device=dev), SF_TILED if tiled else SF_LINEAR, _stream(stream)))
+    return q, sf, r
 
 
 # ------------------------------------------------------------------ MXFP4 (use_nvfp4=False)

@@ -18,8 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libnvfp4.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["api.cu", "gemm.cu", "quantize.cu", "moe.cu", "noalloc.cu"]
-HEADERS = ["ptx.cuh", "gemm_kernel.cuh", "internal.h", "quant_core.cuh"]
+SOURCES = ["api.cu", "gemm.cu", "gemm_fused.cu", "quantize.cu", "moe.cu", "norm.cu",
+           "noalloc.cu"]
+HEADERS = ["ptx.cuh", "gemm_kernel.cuh", "gemm_epilogue.cuh", "gemm_launch.cuh", "internal.h", "quant_core.cuh"]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",

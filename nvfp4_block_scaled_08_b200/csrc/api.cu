@@ -106,6 +106,66 @@ nvfp4_status check_gemm_common(const void* A, const void* sfA, const void* B, co
     return static_cast<nvfp4_status>(nvfp4::check_gemm_args(A, sfA, B, sfB, alpha, out, N, K));
 }
 
+bool valid_out_dtype(nvfp4_out_dtype t) { return t == NVFP4_OUT_BF16 || t == NVFP4_OUT_F16 || t == NVFP4_OUT_F32; }
+bool valid_act(nvfp4_act a) { return a >= NVFP4_ACT_NONE && a <= NVFP4_ACT_RELU2; }
+
+// The rest of every fused product: plan (no workspace), launch. L holds all but the error word.
+nvfp4_status launch_fused(nvfp4::GemmLaunch& L, int epilogue, cudaStream_t stream)
+{
+    DeviceInfo d;
+    nvfp4_status st = current_device(&d);
+    if (st != NVFP4_OK) return st;
+    const nvfp4::GemmPlan plan = nvfp4::plan_gemm(L.M, L.N, L.K, false, d.num_sms);
+    // tiled scales: Q tiles start on 128-row tile boundaries (tuning overrides can break it)
+    if (plan.swap ? plan.q_tiles != 1 : (plan.bn % 128 != 0)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    L.err_word = d.err_word;
+    bool enc_failed = false;
+    const cudaError_t e = nvfp4::launch_gemm_fused(plan, L, epilogue, stream, &enc_failed);
+    if (enc_failed) return NVFP4_ERR_CUDA;
+    return from_cuda(e);
+}
+
+// Checks of the gated products' shapes and operands; `io` is any required 16-byte aligned array.
+nvfp4_status check_glu(const void* A, const void* sfA, const void* B, const void* sfB, const void* alpha,
+                       const void* io, int64_t M, int64_t I, int64_t K)
+{
+    if (M > kMaxDim || I > kMaxDim / 2 || I % 32 != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    return check_gemm_common(A, sfA, B, sfB, alpha, io, 2 * I, K);
+}
+
+// Checks shared by the two residual norms; `out`: out or q.
+nvfp4_status check_norm(const nvfp4::NormLaunch& a, int64_t rows, int64_t H, nvfp4_out_dtype dtype, nvfp4_norm norm,
+                        const void* out)
+{
+    if (rows < 0 || H < 0 || !valid_out_dtype(dtype) || (norm != NVFP4_NORM_RMS && norm != NVFP4_NORM_LAYER) ||
+        !(a.eps >= 0.0f))
+        return NVFP4_ERR_INVALID_ARG;
+    if (rows == 0 || H == 0) return NVFP4_OK;
+    if (!a.x || !a.w || !out || (!a.y && (a.post || a.gate || a.r))) return NVFP4_ERR_INVALID_ARG;
+    if (H % 8 != 0 || H > nvfp4::kMaxNormH || rows > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (a.ld_x < H || (a.y && a.ld_y < H) || (a.r && a.ld_r < H)) return NVFP4_ERR_INVALID_ARG;
+    const int64_t per16 = dtype == NVFP4_OUT_F32 ? 4 : 8;      // elements in 16 bytes
+    if (!aligned16(a.x) || !aligned16(a.y) || !aligned16(a.r) || !aligned16(a.w) || !aligned16(a.b) ||
+        !aligned16(a.post) || !aligned16(a.gate) || !aligned16(out) || a.ld_x % per16 != 0 ||
+        (a.y && a.ld_y % per16 != 0) || (a.r && a.ld_r % per16 != 0))
+        return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+nvfp4_status launch_norm(nvfp4::NormLaunch& a, int64_t rows, int64_t H, nvfp4_out_dtype dtype, nvfp4_norm norm,
+                         cudaStream_t stream)
+{
+    DeviceInfo d;
+    nvfp4_status st = current_device(&d);
+    if (st != NVFP4_OK) return st;
+    a.rows = rows;
+    a.H = static_cast<int32_t>(H);
+    a.dtype = static_cast<int32_t>(dtype);
+    a.layer = norm == NVFP4_NORM_LAYER ? 1 : 0;
+    a.inv_h = static_cast<float>(1.0 / static_cast<double>(H));
+    return from_cuda(nvfp4::launch_residual_norm(a, stream, d.num_sms));
+}
+
 }  // namespace
 
 namespace nvfp4 {
@@ -328,6 +388,129 @@ nvfp4_status nvfp4_gemm_ex2(const uint8_t* A, const uint8_t* sfA, const uint8_t*
                             cudaStream_t stream)
 {
     return nvfp4_gemm_ex3(A, sfA, B, sfB, alpha, out, M, N, K, ws, ws_bytes, sf_layout, out_dtype, 0u, stream);
+}
+
+nvfp4_status nvfp4_gemm_epilogue(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                                 const float* alpha, void* out, int64_t M, int64_t N, int64_t K,
+                                 const float* bias, nvfp4_act act, const void* residual, float residual_scale,
+                                 nvfp4_out_dtype out_dtype, uint32_t flags, cudaStream_t stream)
+{
+    if (M < 0 || N < 0 || K < 0 || !valid_out_dtype(out_dtype) || !valid_act(act)) return NVFP4_ERR_INVALID_ARG;
+    if ((flags & ~static_cast<uint32_t>(NVFP4_GEMM_B_READY)) != 0) return NVFP4_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return NVFP4_OK;
+    if (M > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    const nvfp4_status st = check_gemm_common(A, sfA, B, sfB, alpha, out, N, K);
+    if (st != NVFP4_OK) return st;
+    if (!aligned16(bias) || !aligned16(residual)) return NVFP4_ERR_MISALIGNED;
+    nvfp4::GemmLaunch L{A, sfA, B, sfB, alpha, out, M, N, K, nullptr, 0, 0, nullptr, nullptr, true,
+                        static_cast<int32_t>(out_dtype)};
+    L.b_ready = (flags & NVFP4_GEMM_B_READY) != 0;
+    L.act_fn = static_cast<int32_t>(act);
+    L.bias = bias;
+    L.side = residual;
+    L.side_scale = residual_scale;
+    return launch_fused(L, nvfp4::kEpiLinear, stream);
+}
+
+nvfp4_status nvfp4_gate_up_sf_tile(const uint8_t* sf, int64_t I, int64_t K, uint8_t* out, cudaStream_t stream)
+{
+    if (I < 0 || K < 0) return NVFP4_ERR_INVALID_ARG;
+    if (I == 0 || K == 0) return NVFP4_OK;
+    if (!sf || !out) return NVFP4_ERR_INVALID_ARG;
+    if (I % 16 != 0 || K % 64 != 0 || K > kMaxDim || I > kMaxDim / 2) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    DeviceInfo d;
+    nvfp4_status st = current_device(&d);
+    if (st != NVFP4_OK) return st;
+    return from_cuda(nvfp4::launch_gate_up_sf_tile(sf, I, K, out, stream, d.num_sms));
+}
+
+nvfp4_status nvfp4_gemm_glu(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                            const float* alpha, void* h, int64_t M, int64_t I, int64_t K, nvfp4_act act,
+                            nvfp4_out_dtype out_dtype, uint32_t flags, cudaStream_t stream)
+{
+    if (M < 0 || I < 0 || K < 0 || !valid_out_dtype(out_dtype) || !valid_act(act)) return NVFP4_ERR_INVALID_ARG;
+    if ((flags & ~static_cast<uint32_t>(NVFP4_GEMM_B_READY)) != 0) return NVFP4_ERR_INVALID_ARG;
+    if (M == 0 || I == 0) return NVFP4_OK;
+    const nvfp4_status st = check_glu(A, sfA, B, sfB, alpha, h, M, I, K);
+    if (st != NVFP4_OK) return st;
+    nvfp4::GemmLaunch L{A, sfA, B, sfB, alpha, h, M, 2 * I, K, nullptr, 0, 0, nullptr, nullptr, true,
+                        static_cast<int32_t>(out_dtype)};
+    L.b_ready = (flags & NVFP4_GEMM_B_READY) != 0;
+    L.act_fn = static_cast<int32_t>(act);
+    return launch_fused(L, nvfp4::kEpiGlu, stream);
+}
+
+nvfp4_status nvfp4_gemm_glu_quantize(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                                     const float* alpha, int64_t M, int64_t I, int64_t K, nvfp4_act act,
+                                     const float* gs_h, uint8_t* h_q, uint8_t* h_sf, nvfp4_sf_layout h_sf_layout,
+                                     uint32_t flags, cudaStream_t stream)
+{
+    if (M < 0 || I < 0 || K < 0 || !valid_act(act)) return NVFP4_ERR_INVALID_ARG;
+    if (h_sf_layout != NVFP4_SF_LINEAR && h_sf_layout != NVFP4_SF_TILED) return NVFP4_ERR_INVALID_ARG;
+    if ((flags & ~static_cast<uint32_t>(NVFP4_GEMM_B_READY)) != 0) return NVFP4_ERR_INVALID_ARG;
+    if (M == 0 || I == 0) return NVFP4_OK;
+    if (!gs_h || !h_sf) return NVFP4_ERR_INVALID_ARG;
+    if (h_sf_layout == NVFP4_SF_TILED && I % 64 != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    const nvfp4_status st = check_glu(A, sfA, B, sfB, alpha, h_q, M, I, K);
+    if (st != NVFP4_OK) return st;
+    if (!aligned16(h_sf) || !aligned4(gs_h)) return NVFP4_ERR_MISALIGNED;
+    nvfp4::GemmLaunch L{A, sfA, B, sfB, alpha, nullptr, M, 2 * I, K, nullptr, 0, 0, nullptr, nullptr, true, 0,
+                        h_q, h_sf, gs_h};
+    L.b_ready = (flags & NVFP4_GEMM_B_READY) != 0;
+    L.act_fn = static_cast<int32_t>(act);
+    L.h_sf_tiled = h_sf_layout == NVFP4_SF_TILED;
+    return launch_fused(L, nvfp4::kEpiGluQuant, stream);
+}
+
+nvfp4_status nvfp4_gemm_glu_backward(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
+                                     const float* alpha, const void* dh, void* dgu, int64_t M, int64_t I, int64_t K,
+                                     nvfp4_act act, nvfp4_out_dtype dtype, uint32_t flags, cudaStream_t stream)
+{
+    if (M < 0 || I < 0 || K < 0 || !valid_out_dtype(dtype) || !valid_act(act)) return NVFP4_ERR_INVALID_ARG;
+    if ((flags & ~static_cast<uint32_t>(NVFP4_GEMM_B_READY)) != 0) return NVFP4_ERR_INVALID_ARG;
+    if (M == 0 || I == 0) return NVFP4_OK;
+    if (!dh) return NVFP4_ERR_INVALID_ARG;
+    const nvfp4_status st = check_glu(A, sfA, B, sfB, alpha, dgu, M, I, K);
+    if (st != NVFP4_OK) return st;
+    if (!aligned16(dh)) return NVFP4_ERR_MISALIGNED;
+    nvfp4::GemmLaunch L{A, sfA, B, sfB, alpha, dgu, M, 2 * I, K, nullptr, 0, 0, nullptr, nullptr, true,
+                        static_cast<int32_t>(dtype)};
+    L.b_ready = (flags & NVFP4_GEMM_B_READY) != 0;
+    L.act_fn = static_cast<int32_t>(act);
+    L.side = dh;
+    return launch_fused(L, nvfp4::kEpiGluGrad, stream);
+}
+
+nvfp4_status nvfp4_residual_norm(const void* x, const void* y, nvfp4_out_dtype dtype, int64_t rows, int64_t H,
+                                 int64_t ld_x, int64_t ld_y, nvfp4_norm norm, const float* weight, const float* bias,
+                                 const float* post_weight, const float* gate, float residual_scale, float eps,
+                                 void* r_out, int64_t ld_r, void* out, nvfp4_out_dtype out_dtype,
+                                 cudaStream_t stream)
+{
+    nvfp4::NormLaunch a{x, y, ld_x, ld_y, ld_r, r_out, 0, 0, 0, 0, weight, bias, post_weight, gate,
+                        residual_scale, eps, 0.0f, out, static_cast<int32_t>(out_dtype), nullptr, nullptr, nullptr, 0};
+    if (!valid_out_dtype(out_dtype)) return NVFP4_ERR_INVALID_ARG;
+    const nvfp4_status st = check_norm(a, rows, H, dtype, norm, out);
+    if (st != NVFP4_OK || rows == 0 || H == 0) return st;
+    return launch_norm(a, rows, H, dtype, norm, stream);
+}
+
+nvfp4_status nvfp4_residual_norm_quantize(const void* x, const void* y, nvfp4_out_dtype dtype, int64_t rows,
+                                          int64_t H, int64_t ld_x, int64_t ld_y, nvfp4_norm norm,
+                                          const float* weight, const float* bias, const float* post_weight,
+                                          const float* gate, float residual_scale, float eps, void* r_out,
+                                          int64_t ld_r, const float* gs, uint8_t* q, uint8_t* sf,
+                                          nvfp4_sf_layout sf_layout, cudaStream_t stream)
+{
+    nvfp4::NormLaunch a{x, y, ld_x, ld_y, ld_r, r_out, 0, 0, 0, 0, weight, bias, post_weight, gate,
+                        residual_scale, eps, 0.0f, nullptr, 0, q, sf, gs, sf_layout == NVFP4_SF_TILED ? 1 : 0};
+    if (sf_layout != NVFP4_SF_LINEAR && sf_layout != NVFP4_SF_TILED) return NVFP4_ERR_INVALID_ARG;
+    const nvfp4_status st = check_norm(a, rows, H, dtype, norm, q);
+    if (st != NVFP4_OK || rows == 0 || H == 0) return st;
+    if (!gs || !sf) return NVFP4_ERR_INVALID_ARG;
+    if (H % 16 != 0 || (sf_layout == NVFP4_SF_TILED && H % 64 != 0)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(sf) || !aligned4(gs)) return NVFP4_ERR_MISALIGNED;
+    return launch_norm(a, rows, H, dtype, norm, stream);
 }
 
 nvfp4_status nvfp4_mx_quantize(const void* x, nvfp4_in_dtype dtype, int64_t rows, int64_t K, int64_t ld_x,

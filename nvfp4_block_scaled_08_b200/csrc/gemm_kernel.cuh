@@ -100,11 +100,16 @@ struct GemmArgs {
     uint8_t* h_q;             // SWIGLU: NVFP4 codes of h [total_rows, I/2]
     uint8_t* h_sf;            // SWIGLU: e4m3 scales of h [total_rows, I/16]
     const float* gs_h;        // SWIGLU: global scale of h (device, 1)
-    int32_t inter;            // SWIGLU: I (gate rows = up rows), N = 2 I
+    int32_t inter;            // SWIGLU, GLU: I (gate rows = up rows), N = 2 I
+    int32_t act_fn;           // EPI: activation (nvfp4_act)
+    const float* bias;        // kEpiLinear: [N], or null
+    const void* side;         // kEpiLinear: residual [M][N] or null; kEpiGluGrad: dh [M][I]; out_dtype elements
+    float side_scale;         // kEpiLinear: residual_scale
+    int32_t h_sf_tiled;       // kEpiGluQuant: h_sf in the tiled layout (1) or row-major (0)
 };
 
 template <int BN_, bool SWAP_, bool GROUPED_, bool SFT_ = false, bool SWIGLU_ = false, bool MX_ = false,
-          bool PAIR_ = false, bool ACTQ_ = false>
+          bool PAIR_ = false, bool ACTQ_ = false, int EPI_ = kEpiPlain>
 struct GemmCfg {
     static constexpr int BN = BN_;
     static constexpr bool SWAP = SWAP_;
@@ -155,6 +160,14 @@ struct GemmCfg {
     static constexpr bool ACTQ = ACTQ_;
     static_assert(!ACTQ || (SWAP && !GROUPED && SFT && !MX && !PAIR && BN <= 64),
                   "in-kernel activation quantisation serves the few-token NVFP4 launches");
+    // EPI: fused epilogue of a dense NVFP4 product with tiled scales. GLU: the weight operand B
+    // holds gate rows [0, I) then up rows [I, 2I) and is read through a 5-D view that interleaves
+    // 16 gate rows with the 16 up rows of the same index, so every 32 rows of a weight tile are
+    // the (g, u) pairs of one 16-element block of h; its tiled scales are stored in that order.
+    static constexpr int EPI = EPI_;
+    static constexpr bool GLU = EPI >= kEpiGlu;
+    static_assert(EPI == kEpiPlain || (SFT && !GROUPED && !MX && !ACTQ && !(PAIR && BN != 256)),
+                  "fused epilogues serve the dense NVFP4 product with tiled scales");
     static constexpr int ACTQ_BYTES = ACTQ ? 1024 + 64 + 64 : 0;   // gs / e4m3 table, maxima slots, reduction
     static_assert(!SFT || BN % 128 == 0 || (SWAP && BN <= 64), "Q tiles on 128-row tile boundaries");
     static_assert(!GROUPED || SWAP, "grouped GEMM runs with weights as the MMA M operand");
@@ -205,12 +218,16 @@ struct GemmCfg {
     // and a 16-byte scale stage
     static constexpr int SWIGLU_BYTES = SWIGLU ? 1024 + kEpilogueWarps * (128 + 16) : 0;
     // split-K receive buffer: this rank's chunk (at most ceil(16 / cs) * 8 rows) from each of
-    // cs <= 8 ranks, cs * ceil(16 / cs) * 8 <= 168 rows of [BN + 4] floats. Few-token (swap)
+    // cs <= 8 ranks, cs * ceil(16 / cs) * 8 <= 168 rows of [BN + 4] floats; where weights are the
+    // MMA M operand of a GLU, whole 32-row (g, u) groups: cs * ceil(4 / cs) * 32 <= 256 rows.
+    // Few-token (swap)
     // launches give it a region of its own (RX_OWN), so that the cluster barrier before the
     // exchange moves into the prologue; other split-K launches reuse the drained stage ring.
     static constexpr int PSTRIDE = BN + 4;
     static constexpr bool RX_OWN = SWAP && !GROUPED;
-    static constexpr int RX_BYTES = RX_OWN ? ((168 * PSTRIDE * 4 + 1023) & ~1023) : 0;
+    static constexpr int CHUNK_ROWS = GLU && SWAP ? 32 : 8;   // rows that stay together
+    static constexpr int RX_ROWS = CHUNK_ROWS == 32 ? 256 : 168;
+    static constexpr int RX_BYTES = RX_OWN ? ((RX_ROWS * PSTRIDE * 4 + 1023) & ~1023) : 0;
     static constexpr int MISC_BYTES = 1024 + (GROUPED ? 4 * (kMaxExperts + 1) : 0) + SWIGLU_BYTES + RX_BYTES +
                                       ACTQ_BYTES;
     static constexpr int ALIGN_SLACK = 1024;
@@ -238,7 +255,7 @@ struct GemmCfg {
     static constexpr int OFF_ACTQ = OFF_RX + RX_BYTES;
     static constexpr int SMEM_BYTES = OFF_ACTQ + ACTQ_BYTES + ALIGN_SLACK;
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
-    static_assert(RX_OWN || 168 * PSTRIDE * 4 <= STAGES * STAGE_BYTES, "split-K receive buffer fits the pipeline buffers");
+    static_assert(RX_OWN || RX_ROWS * PSTRIDE * 4 <= STAGES * STAGE_BYTES, "split-K receive buffer fits the pipeline buffers");
     static_assert(OFF_Q % 1024 == 0 && OFF_SFP % 1024 == 0, "swizzle atoms need 1 KB alignment");
 };
 
@@ -564,11 +581,21 @@ __device__ __forceinline__ void store_rows64(const GemmArgs& a, const Tile& ti, 
     }
 }
 
-// Rows [chunk_begin(k), chunk_begin(k + 1)) of a 128-row tile belong to cluster rank k:
-// whole 8-row groups, as evenly as possible (at most ceil(16 / cs) * 8 rows per rank).
-__device__ __forceinline__ int chunk_begin(int k, int cs) { return ((k * 16 + cs - 1) / cs) * 8; }
+// Rows [chunk_begin(k), chunk_begin(k + 1)) of a 128-row tile belong to cluster rank k: whole
+// groups of CHUNK_ROWS rows, as evenly as possible (8-row groups: at most ceil(16 / cs) * 8 rows
+// per rank; 32-row groups: at most ceil(4 / cs) * 32, and some ranks of cs > 4 have none).
+template <class Cfg>
+__device__ __forceinline__ int chunk_begin(int k, int cs)
+{
+    constexpr int UNITS = 128 / Cfg::CHUNK_ROWS;
+    return ((k * UNITS + cs - 1) / cs) * Cfg::CHUNK_ROWS;
+}
 // The rank whose chunk holds `row`.
-__device__ __forceinline__ int chunk_owner(int row, int cs) { return ((row >> 3) * cs) >> 4; }
+template <class Cfg>
+__device__ __forceinline__ int chunk_owner(int row, int cs)
+{
+    return (row / Cfg::CHUNK_ROWS) * cs / (128 / Cfg::CHUNK_ROWS);
+}
 
 // Writes a reduced chunk of a tile: rows [r0, r0 + rows) of the 128 x BN accumulator tile,
 // each the in-order sum of `nsrc` fp32 copies in shared memory (copy j, chunk row lr, column
@@ -817,6 +844,20 @@ __device__ __forceinline__ float actq_quantize_t(const GemmArgs& a, uint8_t* sme
     return alpha;
 }
 
+// The fused epilogues (EPI), defined in gemm_epilogue.cuh, which every translation unit that
+// instantiates them includes. epi_rows64: 64 accumulator columns c0 .. c0 + 63 of a warp's 32 rows
+// (non-swap tiles, lane = token row); epi_tok16: 16 columns (tokens) of a warp's 32 weight rows
+// (swap tiles); epi_chunk: a reduced split-K chunk, in the terms of store_chunk.
+template <class Cfg>
+__device__ __forceinline__ void epi_rows64(const GemmArgs& a, const Tile& ti, int quad, int lane, int c0,
+                                           const uint32_t (&r)[4][16], float alpha);
+template <class Cfg>
+__device__ __forceinline__ void epi_tok16(const GemmArgs& a, const Tile& ti, int quad, int lane, int c,
+                                          const uint32_t (&r)[16], float alpha);
+template <class Cfg>
+__device__ __forceinline__ void epi_chunk(const GemmArgs& a, const Tile& ti, const float* src, int nsrc, int r0,
+                                          int rows, int tid, float alpha);
+
 // Split-K epilogue of one CTA, run by the 128 threads of the first epilogue warpgroup
 // (thread = accumulator row; named barrier 2);
 // every CTA of a split-K launch owns exactly one tile. The `cluster_size` CTAs of a cluster
@@ -842,18 +883,18 @@ __device__ __forceinline__ void split_k_epilogue(const GemmArgs& a, const Tile& 
     const int cs = a.cluster_size;
     const int g = a.groups;
     const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int owner = chunk_owner(row, cs);
+    const int owner = chunk_owner<Cfg>(row, cs);
     float* rx = reinterpret_cast<float*>(smem + (Cfg::RX_OWN ? Cfg::OFF_RX : Cfg::OFF_P));
     // the receive buffer aliases the stage ring: wait until every CTA of the cluster has drained
     // its main loop (with a region of its own, the prologue's cluster barrier covered it)
     if (!Cfg::RX_OWN && cs > 1) { cluster_arrive(); cluster_wait(); }
 
-    const int my0 = chunk_begin(rank, cs);
-    const int my_rows = chunk_begin(rank + 1, cs) - my0;
+    const int my0 = chunk_begin<Cfg>(rank, cs);
+    const int my_rows = chunk_begin<Cfg>(rank + 1, cs) - my0;
     const int grp = ti.split / cs;
     const bool is_owner = owner == rank;
-    const int own0 = chunk_begin(owner, cs);
-    const int own_rows = chunk_begin(owner + 1, cs) - own0;
+    const int own0 = chunk_begin<Cfg>(owner, cs);
+    const int own_rows = chunk_begin<Cfg>(owner + 1, cs) - own0;
 
     // 1. every row to slot `rank` of its owner's receive buffer. tcgen05.ld is .sync.aligned:
     //    every lane of the warp executes every load, only the destination depends on the row.
@@ -878,7 +919,7 @@ __device__ __forceinline__ void split_k_epilogue(const GemmArgs& a, const Tile& 
     //    the named barrier publishes the own-slot rows to all 128 threads
     bool ok = true;
     if (cs > 1) {
-        if (row == my0)
+        if (row == 0)
             mbar_arrive_expect_tx(rx_bar, static_cast<uint32_t>((cs - 1) * my_rows * BN * 4));
         ok = mbar_wait(rx_bar, 0, ab, kErrSplitRx);
     }
@@ -887,6 +928,10 @@ __device__ __forceinline__ void split_k_epilogue(const GemmArgs& a, const Tile& 
     if (!ok) return;
 
     // 3. reduce over the ranks in order
+    if constexpr (Cfg::EPI != kEpiPlain) {       // never launched with a workspace (g == 1)
+        epi_chunk<Cfg>(a, ti, rx, cs, my0, my_rows, row, alpha);
+        return;
+    }
     if (g == 1) {
         store_chunk<Cfg>(a, ti, rx, cs, my0, my_rows, row, alpha);
         return;
@@ -970,12 +1015,14 @@ __device__ __forceinline__ void sft_stage_copies(const GemmArgs& a, const Tile& 
         mbar_arrive_expect_tx(fb, Cfg::P_BYTES + Cfg::SFP_BYTES + q_bytes);
     }
     if (do_p) {
-        tma_load_2d(pbuf, tm_p, fb, kx, ti.p0, pol_p);
+        if constexpr (Cfg::GLU && Cfg::SWAP) tma_load_5d(pbuf, tm_p, fb, kx, 0, 0, ti.p0 >> 5, 0, pol_p);
+        else tma_load_2d(pbuf, tm_p, fb, kx, ti.p0, pol_p);
         bulk_load(sfpb, a.sf_p + ((ti.p0 >> 7) * static_cast<int64_t>(a.sf_kb4) + kb) * 512, Cfg::SFP_BYTES, fb,
                   pol_p);
     }
     if (do_q) {
-        tma_load_2d(qbuf, tm_q, fb, kx, ti.q0, pol_q);
+        if constexpr (Cfg::GLU && !Cfg::SWAP) tma_load_5d(qbuf, tm_q, fb, kx, 0, 0, ti.q0 >> 5, 0, pol_q);
+        else tma_load_2d(qbuf, tm_q, fb, kx, ti.q0, pol_q);
         for (int g = 0; g < ng; ++g)
             bulk_load(sfqb + Cfg::SFP_BYTES * g,
                       a.sf_q + (((ti.q0 >> 7) + g) * static_cast<int64_t>(a.sf_kb4) + kb) * 512, Cfg::SFP_BYTES,
@@ -1150,7 +1197,13 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
                 const int n = ti.kcnt < STAGES ? ti.kcnt : STAGES;
                 for (int ks = 0; ks < n; ++ks) {
                     const int32_t kx = (ti.k0 + ks) * Cfg::BK_BYTES;
-                    if constexpr (Cfg::SWAP) tma_prefetch_2d(&tm_p, kx, ti.p0);
+                    if constexpr (Cfg::GLU) {
+                        const int32_t w0 = Cfg::SWAP ? ti.p0
+                                         : Cfg::PAIR ? ti.q0 + (ti.q_span / 2) * static_cast<int32_t>(cluster_ctarank())
+                                                     : ti.q0;
+                        tma_prefetch_5d(Cfg::SWAP ? &tm_p : &tm_q, kx, 0, 0, w0 >> 5, 0);
+                    }
+                    else if constexpr (Cfg::SWAP) tma_prefetch_2d(&tm_p, kx, ti.p0);
                     else if constexpr (Cfg::PAIR) tma_prefetch_2d(&tm_q, kx, ti.q0 + (ti.q_span / 2) * static_cast<int32_t>(cluster_ctarank()));
                     else tma_prefetch_2d(&tm_q, kx, ti.q0);
                 }
@@ -1238,8 +1291,11 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
                         const int32_t kb = Cfg::SF_BLOCKS * (ti.k0 + ks);
                         const int32_t kb4 = args.sf_kb4;
                         tma_load_2d_pair(pbuf, &tm_p, fb0, kx, ti.p0, pol_p);
-                        tma_load_2d_pair(qbuf, narrow ? &tm_q_half : &tm_q, fb0, kx,
-                                         ti.q0 + (ti.q_span / 2) * static_cast<int32_t>(rank), pol_q);
+                        const int32_t q0 = ti.q0 + (ti.q_span / 2) * static_cast<int32_t>(rank);
+                        if constexpr (Cfg::GLU)
+                            tma_load_5d_pair(qbuf, narrow ? &tm_q_half : &tm_q, fb0, kx, 0, 0, q0 >> 5, 0, pol_q);
+                        else
+                            tma_load_2d_pair(qbuf, narrow ? &tm_q_half : &tm_q, fb0, kx, q0, pol_q);
                         tma_load_2d_pair(sfpb, &tm_sfp, fb0, 0, ((ti.p0 >> 7) * kb4 + kb) * 2, pol_p);
 #pragma unroll
                         for (int g = 0; g < QG; ++g)
@@ -1533,7 +1589,9 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
                         else mbar_arrive_relaxed(&sf_free_bar[acc]);
                     }
                     if (need) {
-                        if constexpr (!Cfg::SWAP && !Cfg::GROUPED) {
+                        if constexpr (Cfg::EPI != kEpiPlain) {
+                            epi_rows64<Cfg>(args, ti, quad, lane, BN - 64, r, alpha);
+                        } else if constexpr (!Cfg::SWAP && !Cfg::GROUPED) {
                             store_rows64<Cfg>(args, ti, quad, lane, BN - 64, r, alpha);
                         } else if constexpr (Cfg::SWIGLU) {
 #pragma unroll
@@ -1564,10 +1622,12 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x16(tacc + c0 + 16 * i, r[i]);
                     tmem_ld_wait();
-                    store_rows64<Cfg>(args, ti, quad, lane, c0, r, alpha);
+                    if constexpr (Cfg::EPI != kEpiPlain) epi_rows64<Cfg>(args, ti, quad, lane, c0, r, alpha);
+                    else store_rows64<Cfg>(args, ti, quad, lane, c0, r, alpha);
                 }
                 // the rest (BN = 224, 192: 48, 32 columns per half) the plain way
-                for (; c0 < c_hi; c0 += 16) {
+                static_assert(Cfg::EPI == kEpiPlain || BN % 128 == 0, "fused epilogues take whole 64-column chunks");
+                for (; Cfg::EPI == kEpiPlain && c0 < c_hi; c0 += 16) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(tacc + c0, r);
                     tmem_ld_wait();
@@ -1585,7 +1645,9 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
                     for (int h = 0; h < 2; ++h) {
                         if (h == 1 && !two) break;
                         const int c = c0 + 16 * h;
-                        if constexpr (Cfg::SWIGLU)
+                        if constexpr (Cfg::EPI != kEpiPlain)
+                            epi_tok16<Cfg>(args, ti, quad, lane, c, r[h], alpha);
+                        else if constexpr (Cfg::SWIGLU)
                             swiglu_chunk16<Cfg>(args, ti, quad, lane, c, r[h], alpha, gsh, rcp_tab, stage_w, sstage_w);
                         else if (args.out_dtype != kOutF32)
                             store_tok16<Cfg>(args, ti, quad, lane, c, r[h], alpha);

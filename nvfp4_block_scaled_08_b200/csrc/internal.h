@@ -34,6 +34,10 @@ cudaError_t launch_moe_route(const float* logits, int32_t T, int32_t E, int32_t 
 cudaError_t launch_moe_combine(const void* y, int32_t y_dt, const float* weights, const int32_t* row_of,
                                int32_t T, int64_t H, int32_t k, void* out, int32_t out_dt, cudaStream_t stream,
                                int num_sms);
+// Row-major scales [2 I][K / 16] of gate rows [0, I) and up rows [I, 2 I) -> the tiled layout of the
+// rows in groups of 16 gate rows and their 16 up rows.
+cudaError_t launch_gate_up_sf_tile(const uint8_t* sf, int64_t I, int64_t K, uint8_t* out, cudaStream_t stream,
+                                   int num_sms);
 // Row-major NVFP4 scales [rows][K / 16] -> the 8 x 4 layout.
 cudaError_t launch_sf_8x4(const uint8_t* sf, int64_t rows, int64_t K, uint8_t* out, cudaStream_t stream,
                           int num_sms);
@@ -47,6 +51,24 @@ cudaError_t launch_alpha(const float* gs_a, const float* gs_b, int32_t n, float*
                          cudaStream_t stream);
 cudaError_t launch_round(const float* x, int64_t n, uint8_t* out, bool e2m1, cudaStream_t stream,
                          int num_sms);
+
+// norm.cu: residual add, norms and output (nvfp4_residual_norm, nvfp4_residual_norm_quantize).
+// Largest row the kernel holds in one block's registers.
+constexpr int64_t kMaxNormH = 32768;
+struct NormLaunch {
+    const void* x; const void* y;               // y null: r = x
+    int64_t ld_x, ld_y, ld_r;                   // row strides in elements
+    void* r;                                    // null: r is not stored
+    int64_t rows;
+    int32_t H, dtype;                           // dtype of x, y, r (nvfp4_out_dtype)
+    int32_t layer;                              // layer norm (1) or RMS norm (0)
+    const float *w, *b, *post, *gate;           // [H]; all but w optional
+    float scale, eps, inv_h;
+    void* out; int32_t out_dt;                  // [rows][H], or
+    uint8_t* q; uint8_t* sf; const float* gs;   // NVFP4 codes and scales (q not null)
+    int32_t sf_tiled;
+};
+cudaError_t launch_residual_norm(const NormLaunch& a, cudaStream_t stream, int num_sms);
 
 // Tiling chosen for one GEMM call.
 struct GemmPlan {
@@ -101,6 +123,13 @@ struct GemmLaunch {
     float* gs_out = nullptr;
     float* alpha_out = nullptr;
     bool sf_8x4 = false;        // sfA and sfB in the 8 x 4 layout (dense NVFP4 GEMM only)
+    // fused epilogues (launch_gemm_fused): activation, bias, residual (kEpiLinear) or dh
+    // (kEpiGluGrad) in out_dtype; h_q, h_sf, gs_h above for the quantised gated output
+    int32_t act_fn = 0;
+    const float* bias = nullptr;
+    const void* side = nullptr;
+    float side_scale = 0.0f;
+    bool h_sf_tiled = false;
     bool b_ready = false;       // NVFP4_GEMM_B_READY: B's first stages may load before the
                                 // wait for the previous kernel in the stream
 };
@@ -122,5 +151,20 @@ int act_gemm_stages(int bn);
 // could not be encoded.
 cudaError_t launch_gemm(const GemmPlan& plan, const GemmLaunch& L, cudaStream_t stream,
                         bool* encode_failed);
+
+// What the epilogue of a dense product does with acc (gemm_epilogue.cuh; kEpiPlain: out = alpha *
+// acc, in gemm_kernel.cuh).
+enum : int {
+    kEpiPlain = 0,
+    kEpiLinear = 1,     // out = act(alpha * acc + bias) + side_scale * side
+    kEpiGlu = 2,        // h = act(g) * u in out_dtype
+    kEpiGluQuant = 3,   // h as NVFP4 codes and scales
+    kEpiGluGrad = 4,    // dg = dh * u * act'(g), du = dh * act(g) in out_dtype
+};
+
+// gemm_fused.cu: the dense NVFP4 product with tiled scales and a fused epilogue (other than
+// kEpiPlain). The plan must use no workspace (groups == 1).
+cudaError_t launch_gemm_fused(const GemmPlan& plan, const GemmLaunch& L, int epilogue, cudaStream_t stream,
+                              bool* encode_failed);
 
 }  // namespace nvfp4

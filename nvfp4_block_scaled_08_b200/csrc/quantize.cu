@@ -621,6 +621,31 @@ __global__ void sf_tile_kernel(const uint8_t* __restrict__ sf, int64_t rows, int
     }
 }
 
+// sf_tile_kernel for gate rows [0, I) and up rows [I, 2 I): row r of the output order is gate row
+// 16 (r / 32) + r % 32 where r % 32 < 16, up row I + 16 (r / 32) + r % 32 - 16 otherwise.
+__global__ void gate_up_sf_tile_kernel(const uint8_t* __restrict__ sf, int64_t I, int64_t kb, int64_t kb4,
+                                       uint8_t* __restrict__ out, int64_t out_bytes)
+{
+    for (int64_t o = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; o < out_bytes;
+         o += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t block = o >> 9, within = o & 511;
+        const int64_t rt = block / kb4, kt = block - rt * kb4;
+        const int64_t r = rt * 128 + ((within >> 2) & 3) * 32 + (within >> 4);
+        const int64_t src = (r >> 5) * 16 + (r & 15) + ((r & 16) ? I : 0);
+        out[o] = r < 2 * I ? sf[src * kb + kt * 4 + (within & 3)] : 0;
+    }
+}
+
+cudaError_t launch_gate_up_sf_tile(const uint8_t* sf, int64_t I, int64_t K, uint8_t* out, cudaStream_t stream,
+                                   int num_sms)
+{
+    const int64_t kb = K / 16;
+    const int64_t out_bytes = (2 * I + 127) / 128 * 128 * kb;
+    if (out_bytes == 0) return cudaSuccess;
+    gate_up_sf_tile_kernel<<<grid_for(out_bytes, num_sms), 256, 0, stream>>>(sf, I, kb, kb / 4, out, out_bytes);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_sf_tile(const uint8_t* sf, int64_t rows, int64_t K, uint8_t* out, cudaStream_t stream,
                            int num_sms, int block)
 {
