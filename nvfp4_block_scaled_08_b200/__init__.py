@@ -120,6 +120,8 @@ def library_path() -> str:
 def load(build_if_needed: bool = True) -> ctypes.CDLL:
     """Load libnvfp4.so (compiling it with nvcc first if it is missing or stale)."""
     global _lib
+    if _lib is not None:                 # set once, complete
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -143,8 +145,10 @@ def _check(fn: str, status: int):
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    # the current stream's raw handle (torch.cuda.current_stream() builds a Stream object: 3 us)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _ptr(t: torch.Tensor | None):
@@ -413,27 +417,27 @@ def _code(table: dict, name: str, what: str) -> int:
     return table[name]
 
 
-def _arg(t, name: str, dtype, shape=None, numel=None, device=None) -> int | None:
-    """The address of a contiguous CUDA tensor of this type and shape (or with at least `numel`
-    elements) on `device`; None for None. The kernels trust sizes, so the binding checks them."""
+def _arg(t, name: str, dtype, dev: int, shape=None, numel: int = 0) -> int | None:
+    """The address of a contiguous tensor of this type and shape (or of at least `numel` elements)
+    on CUDA device `dev`; None for None. The kernels trust sizes, so the binding checks them."""
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if numel is not None and t.numel() < numel:
-        raise ValueError(f"{name} needs at least {numel} elements")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
+    if shape is None:
+        if t.numel() < numel:
+            raise ValueError(f"{name} needs at least {numel} elements")
+    elif t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _on_current_device(t: torch.Tensor, name: str):
-    _dev(t, name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    return t.device
+def _current_device(t: torch.Tensor, name: str) -> int:
+    """The index of the current CUDA device, which must be t's."""
+    dev = t.get_device()                 # -1: not a CUDA tensor
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    return dev
 
 
 def _tiled_bytes(rows: int, K: int) -> int:
@@ -441,15 +445,15 @@ def _tiled_bytes(rows: int, K: int) -> int:
 
 
 def _operands(Aq, sfA, Bq, sfB, alpha_t):
-    """Checked addresses of A and B with tiled scales and alpha, and (M, N, K, device)."""
-    dev = _on_current_device(Aq, "Aq")
-    if Aq.dim() != 2 or Bq.dim() != 2 or Aq.shape[1] != Bq.shape[1]:
+    """Checked addresses of A and B with tiled scales and alpha, and (M, N, K, device index)."""
+    dev = _current_device(Aq, "Aq")
+    (M, k2), (N, kb2), u8 = Aq.shape, Bq.shape, torch.uint8
+    if k2 != kb2:
         raise ValueError("Aq and Bq must be [rows, K/2] with the same K")
-    (M, k2), N = Aq.shape, Bq.shape[0]
-    u8, K = torch.uint8, 2 * k2
-    return (_arg(Aq, "Aq", u8), _arg(sfA, "sfA", u8, numel=_tiled_bytes(M, K), device=dev),
-            _arg(Bq, "Bq", u8, device=dev), _arg(sfB, "sfB", u8, numel=_tiled_bytes(N, K), device=dev),
-            _arg(alpha_t, "alpha", torch.float32, numel=1, device=dev)), M, N, K, dev
+    K = 2 * k2
+    return (_arg(Aq, "Aq", u8, dev), _arg(sfA, "sfA", u8, dev, None, _tiled_bytes(M, K)),
+            _arg(Bq, "Bq", u8, dev), _arg(sfB, "sfB", u8, dev, None, _tiled_bytes(N, K)),
+            _arg(alpha_t, "alpha", torch.float32, dev, None, 1)), M, N, K, dev
 
 
 def gemm_epilogue(Aq, sfA, Bq, sfB, alpha_t, out=None, *, bias=None, act: str = "none", residual=None,
@@ -461,11 +465,11 @@ def gemm_epilogue(Aq, sfA, Bq, sfB, alpha_t, out=None, *, bias=None, act: str = 
     dtype, which may be out itself; b_ready as for gemm."""
     ops, M, N, K, dev = _operands(Aq, sfA, Bq, sfB, alpha_t)
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+        out = torch.empty(M, N, dtype=out_dtype, device=Aq.device)
     _check("nvfp4_gemm_epilogue", load().nvfp4_gemm_epilogue(
-        *ops, _arg(out, "out", out.dtype, (M, N), device=dev), M, N, K,
-        _arg(bias, "bias", torch.float32, (N,), device=dev), _code(ACTS, act, "act"),
-        _arg(residual, "residual", out.dtype, (M, N), device=dev), residual_scale, _out_code(out),
+        *ops, _arg(out, "out", out.dtype, dev, (M, N)), M, N, K,
+        _arg(bias, "bias", torch.float32, dev, (N,)), _code(ACTS, act, "act"),
+        _arg(residual, "residual", out.dtype, dev, (M, N)), residual_scale, _out_code(out),
         1 if b_ready else 0, _stream(stream)))
     return out
 
@@ -473,15 +477,15 @@ def gemm_epilogue(Aq, sfA, Bq, sfB, alpha_t, out=None, *, bias=None, act: str = 
 def gate_up_sf_tile(sf: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Row-major scales [2I, K/16] of a gate_up weight (gate rows, then up rows) -> the scales
     that gemm_glu and its relatives take (flat uint8 tensor); once per weight."""
-    dev = _on_current_device(sf, "sf")
+    dev = _current_device(sf, "sf")
     if sf.dim() != 2 or sf.shape[0] % 2:
         raise ValueError("sf must be [2I, K/16]")
     rows, K = sf.shape[0], sf.shape[1] * 16
     if out is None:
         out = torch.empty(_tiled_bytes(rows, K), dtype=torch.uint8, device=dev)
     _check("nvfp4_gate_up_sf_tile", load().nvfp4_gate_up_sf_tile(
-        _arg(sf, "sf", torch.uint8), rows // 2, K,
-        _arg(out, "out", torch.uint8, numel=_tiled_bytes(rows, K), device=dev), _stream(stream)))
+        _arg(sf, "sf", torch.uint8, dev), rows // 2, K,
+        _arg(out, "out", torch.uint8, dev, None, _tiled_bytes(rows, K)), _stream(stream)))
     return out
 
 
@@ -501,7 +505,7 @@ def gemm_glu(Aq, sfA, Bq, sfB, alpha_t, out=None, *, act: str = "silu", out_dtyp
     if out is None:
         out = torch.empty(M, I, dtype=out_dtype, device=dev)
     _check("nvfp4_gemm_glu", load().nvfp4_gemm_glu(
-        *ops, _arg(out, "out", out.dtype, (M, I), device=dev), M, I, K, _code(ACTS, act, "act"),
+        *ops, _arg(out, "out", out.dtype, dev, (M, I)), M, I, K, _code(ACTS, act, "act"),
         _out_code(out), 1 if b_ready else 0, _stream(stream)))
     return out
 
@@ -519,9 +523,9 @@ def gemm_glu_quantize(Aq, sfA, Bq, sfB, alpha_t, gs_h, h_q=None, h_sf=None, *, a
         h_sf = torch.empty(n, dtype=torch.uint8, device=dev)
         h_sf = h_sf if tiled else h_sf.view(M, I // 16)
     _check("nvfp4_gemm_glu_quantize", load().nvfp4_gemm_glu_quantize(
-        *ops, M, I, K, _code(ACTS, act, "act"), _arg(gs_h, "gs_h", torch.float32, numel=1, device=dev),
-        _arg(h_q, "h_q", torch.uint8, (M, I // 2), device=dev),
-        _arg(h_sf, "h_sf", torch.uint8, numel=n, device=dev), SF_TILED if tiled else SF_LINEAR,
+        *ops, M, I, K, _code(ACTS, act, "act"), _arg(gs_h, "gs_h", torch.float32, dev, None, 1),
+        _arg(h_q, "h_q", torch.uint8, dev, (M, I // 2)),
+        _arg(h_sf, "h_sf", torch.uint8, dev, None, n), SF_TILED if tiled else SF_LINEAR,
         1 if b_ready else 0, _stream(stream)))
     return h_q, h_sf
 
@@ -534,29 +538,41 @@ def gemm_glu_backward(Aq, sfA, Bq, sfB, alpha_t, dh, out=None, *, act: str = "si
     if out is None:
         out = torch.empty(M, 2 * I, dtype=dh.dtype, device=dev)
     _check("nvfp4_gemm_glu_backward", load().nvfp4_gemm_glu_backward(
-        *ops, _arg(dh, "dh", out.dtype, (M, I), device=dev),
-        _arg(out, "out", out.dtype, (M, 2 * I), device=dev), M, I, K, _code(ACTS, act, "act"),
+        *ops, _arg(dh, "dh", out.dtype, dev, (M, I)),
+        _arg(out, "out", out.dtype, dev, (M, 2 * I)), M, I, K, _code(ACTS, act, "act"),
         _out_code(out), 1 if b_ready else 0, _stream(stream)))
     return out
 
 
+def _rows(t, name: str, like):
+    """Address and row stride (elements) of a [rows, H] tensor like x with unit column stride."""
+    if t is None:
+        return None, 0
+    shape, dtype, dev = like
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must have x's shape, type and device")
+    ld, col = t.stride()
+    if col != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
 def _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out):
     """The leading arguments of both residual norms, and r (allocated where y asks for it)."""
-    dev = _on_current_device(x, "x")
+    dev = _current_device(x, "x")
     if x.dim() != 2 or x.dtype not in OUT_DTYPES:
         raise ValueError("x must be [rows, H] in bfloat16, float16 or float32")
     rows, H = x.shape
     if y is not None and r_out is None:
-        r_out = torch.empty(rows, H, dtype=x.dtype, device=dev)
-    for t, name in ((x, "x"), (y, "y"), (r_out, "r_out")):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != dev or (H > 1 and t.stride(1) != 1)):
-            raise ValueError(f"{name} must be like x, with unit column stride")
-    f32 = torch.float32
-    vec = [_arg(t, name, f32, (H,), device=dev) for t, name in
-           ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (gate, "gate"))]
-    ld = [0 if t is None else t.stride(0) if rows > 1 else H for t in (x, y, r_out)]
-    args = (x.data_ptr(), _ptr(y), OUT_DTYPES[x.dtype], rows, H, ld[0], ld[1], _code(NORMS, kind, "kind"), *vec,
-            residual_scale, eps, _ptr(r_out), ld[2])
+        r_out = torch.empty(rows, H, dtype=x.dtype, device=x.device)
+    f32, like = torch.float32, (x.shape, x.dtype, dev)
+    px, ld_x = _rows(x, "x", like)
+    py, ld_y = _rows(y, "y", like)
+    pr, ld_r = _rows(r_out, "r_out", like)
+    args = (px, py, OUT_DTYPES[x.dtype], rows, H, ld_x, ld_y, _code(NORMS, kind, "kind"),
+            _arg(weight, "weight", f32, dev, (H,)), _arg(bias, "bias", f32, dev, (H,)),
+            _arg(post_weight, "post_weight", f32, dev, (H,)), _arg(gate, "gate", f32, dev, (H,)),
+            residual_scale, eps, pr, ld_r)
     return args, (x if y is None else r_out), rows, H, dev
 
 
@@ -571,7 +587,7 @@ def residual_norm(x, weight, y=None, *, kind: str = "rms", bias=None, post_weigh
     if out is None:
         out = torch.empty(rows, H, dtype=out_dtype or x.dtype, device=dev)
     _check("nvfp4_residual_norm", load().nvfp4_residual_norm(
-        *args, _arg(out, "out", out.dtype, (rows, H), device=dev), _out_code(out), _stream(stream)))
+        *args, _arg(out, "out", out.dtype, dev, (rows, H)), _out_code(out), _stream(stream)))
     return out, r
 
 
@@ -589,8 +605,9 @@ def residual_norm_quantize(x, weight, gs, y=None, *, kind: str = "rms", bias=Non
         sf = torch.empty(n, dtype=torch.uint8, device=dev)
         sf = sf if tiled else sf.view(rows, H // 16)
     _check("nvfp4_residual_norm_quantize", load().nvfp4_residual_norm_quantize(
-        *args, _arg(gs, "gs", torch.float32, numel=1, device=dev), _arg(q, "q", torch.uint8, (rows, H // 2), device=dev),
-        _arg(sf, "sf", torch.uint8, numel=n, device=dev), SF_TILED if tiled else SF_LINEAR, _stream(stream)))
+        *args, _arg(gs, "gs", torch.float32, dev, None, 1),
+        _arg(q, "q", torch.uint8, dev, (rows, H // 2)),
+        _arg(sf, "sf", torch.uint8, dev, None, n), SF_TILED if tiled else SF_LINEAR, _stream(stream)))
     return q, sf, r
 
 

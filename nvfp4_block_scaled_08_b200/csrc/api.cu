@@ -115,7 +115,7 @@ nvfp4_status launch_fused(nvfp4::GemmLaunch& L, int epilogue, cudaStream_t strea
     DeviceInfo d;
     nvfp4_status st = current_device(&d);
     if (st != NVFP4_OK) return st;
-    const nvfp4::GemmPlan plan = nvfp4::plan_gemm(L.M, L.N, L.K, false, d.num_sms);
+    const nvfp4::GemmPlan plan = nvfp4::plan_fused(L.M, L.N, L.K, d.num_sms);
     // tiled scales: Q tiles start on 128-row tile boundaries (tuning overrides can break it)
     if (plan.swap ? plan.q_tiles != 1 : (plan.bn % 128 != 0)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     L.err_word = d.err_word;

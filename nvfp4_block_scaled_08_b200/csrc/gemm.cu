@@ -34,6 +34,24 @@ void set_plan_override(int bn, int cluster, int groups, int band, int grouped_bn
 
 static int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
+// The pair launch of a plan whose tiles are set: its grid, band and work items. `halves`: a last
+// wave of 256 x 256 tiles that fills at most half of the pairs runs as twice as many 256 x 128
+// halves, in about half the time (4096^3: 256 tiles on 74 pairs, 3.46 rounds).
+static void plan_pairs(GemmPlan& p, bool halves)
+{
+    const int pairs = ((p.p_tiles + 1) / 2) * p.q_tiles;
+    const int clusters = std::max(1, std::min(pairs, max_active_clusters(2)));
+    p.pair_grid = 2 * clusters;
+    p.pair_band = std::max(1, p.band / 2);
+    const int tail = pairs % clusters;
+    p.pair_items = pairs;
+    p.narrow_from = pairs;
+    if (p.bn == 256 && tail > 0 && 2 * tail <= clusters && halves) {
+        p.narrow_from = pairs - tail;
+        p.pair_items = pairs + tail;
+    }
+}
+
 // Tiling for out[M, N] = A[M, K] x B[N, K]^T on `num_sms` SMs.
 //  * M <= 64: weights fill the 128-row MMA operand (swap), tokens are an MMA N of 16-64.
 //  * otherwise: 128-row token tiles x 128- or 256-row weight tiles, whichever finishes in
@@ -124,22 +142,54 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool allow_workspace, int nu
     const int fp = g_force_pair.load(std::memory_order_relaxed);
     const bool pair_shape = !p.swap && p.splits == 1 && p.p_tiles >= 2;
     p.pair = pair_shape && (((fp == 0 || fp == 3) && p.bn == 256 && nk >= 12) || (fp == 2 && (p.bn == 256 || p.bn == 128)));
-    if (p.pair) {
-        const int pairs = ((p.p_tiles + 1) / 2) * p.q_tiles;
-        const int clusters = std::max(1, std::min(pairs, max_active_clusters(2)));
-        p.pair_grid = 2 * clusters;
-        p.pair_band = std::max(1, p.band / 2);
-        // A last wave of 256 x 256 tiles that fills at most half of the pairs runs as twice
-        // as many 256 x 128 halves, in about half the time (4096^3: 256 tiles on 74 pairs,
-        // 3.46 rounds).
-        const int tail = pairs % clusters;
-        p.pair_items = pairs;
-        p.narrow_from = pairs;
-        if (p.bn == 256 && tail > 0 && 2 * tail <= clusters && fp != 3) {
-            p.narrow_from = pairs - tail;
-            p.pair_items = pairs + tail;
+    if (p.pair) plan_pairs(p, fp != 3);
+    return p;
+}
+
+// The fused products run few-token tiles as the plain product does, and otherwise 128-wide tiles
+// (with or without a split-K cluster) or 256-wide CTA pairs, whichever a model of its measured
+// times puts first. With nk K stages, in us on B200, beside about 3 us per launch:
+//   a round of 256 x 256 pair tiles  0.388 nk + 2.1   (8192 x 4096 x 6144: 7 rounds, 80 measured)
+//   a wave of 128 x 128 tiles        0.30 nk + 1.1    (same: 14 waves, 116; 500 x 2048 x 6144: 11.3)
+//   the same split over cs CTAs      0.30 nk / cs + 4.9  (500 x 2048 x 6144, cs = 2: 11.5)
+// Where they cross: 700 x 4096 x 6144 one round of pairs 14.5, two waves 19.6; 1024 x 6144 x 2048
+// two rounds 11.5, three waves 13.1; 500 x 2048 x 6144 one round 13.2, one wave 11.3.
+GemmPlan plan_fused(int64_t M, int64_t N, int64_t K, int num_sms)
+{
+    GemmPlan p = plan_gemm(M, N, K, false, num_sms);
+    if (p.swap) return p;
+    const int nk = static_cast<int>(K / 256);
+    const int force = g_force_bn.load(std::memory_order_relaxed);
+    const int fc = g_force_cluster.load(std::memory_order_relaxed);
+    const int fp = g_force_pair.load(std::memory_order_relaxed);
+    if (force == 192 || force == 224) return p;          // refused by the caller: linear scales only
+    const int pairs = (p.p_tiles + 1) / 2 * ceil_div(N, 256), clusters = std::max(1, max_active_clusters(2));
+    const int tiles = p.p_tiles * ceil_div(N, 128);
+    int cs = 1;
+    if (fc > 0) {
+        cs = std::min({fc, 8, nk});
+    } else if (tiles * 4 < num_sms * 3) {
+        for (int c = std::min({8, nk, num_sms / tiles}); c >= 2; --c) {
+            if (tiles <= max_active_clusters(c)) { cs = c; break; }
         }
     }
+    const double wave = 0.30 * nk + 1.1, split = 0.30 * nk / cs + 4.9;
+    const double t128 = ceil_div(tiles, num_sms) * wave;
+    if (fc <= 0 && split >= t128) cs = 1;
+    const double t256 = ceil_div(pairs, clusters) * (0.388 * nk + 2.1);
+    // an override of the width, the cluster or the pairs decides what it names
+    bool pair = t256 < (cs > 1 ? split : t128);
+    if (force == 128 || (force == 0 && fc > 1)) pair = false;
+    if (force == 256 || (force == 0 && fp == 2)) pair = true;
+    if (fp == 1 || (fc > 1 && force == 256) || p.p_tiles < 2) pair = false;
+    p.bn = pair ? 256 : 128;
+    p.pair = pair;
+    p.q_tiles = ceil_div(N, p.bn);
+    p.cluster = pair ? 1 : cs;
+    p.splits = p.cluster;
+    p.num_tiles = p.p_tiles * p.q_tiles * p.splits;
+    p.grid = p.splits > 1 ? p.num_tiles : std::min(p.num_tiles, num_sms);
+    if (pair) plan_pairs(p, fp != 3);
     return p;
 }
 
@@ -196,14 +246,14 @@ static std::mutex g_map_mu;
 static std::map<MapKey, CUtensorMap> g_map_cache;
 
 bool get_map_nd(CUtensorMap* out, const void* ptr, int rank, const uint64_t* dims,
-                const uint64_t* strides, const uint32_t* box, bool swizzle128)
+                const uint64_t* strides, const uint32_t* box, int swizzle)
 {
     int dev = 0;
     cudaGetDevice(&dev);
     MapKey key;
     key.v.fill(0);
     key.v[0] = reinterpret_cast<uint64_t>(ptr);
-    key.v[1] = static_cast<uint64_t>(rank) | (swizzle128 ? 0x100ull : 0ull) | (static_cast<uint64_t>(dev) << 16);
+    key.v[1] = static_cast<uint64_t>(rank) | (static_cast<uint64_t>(swizzle) << 8) | (static_cast<uint64_t>(dev) << 16);
     for (int i = 0; i < rank; ++i) {
         key.v[2 + i] = dims[i];
         key.v[7 + i] = box[i];
@@ -232,7 +282,8 @@ bool get_map_nd(CUtensorMap* out, const void* ptr, int rank, const uint64_t* dim
     std::memset(&m, 0, sizeof(m));
     CUresult r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank), const_cast<void*>(ptr), d,
                     st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    swizzle == kSwizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                        : swizzle == kSwizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return false;
     {

@@ -32,6 +32,23 @@ __device__ __forceinline__ void sigmoid_both(float x, float& p, float& q)
 // (1 + tanh z) / 2 = sigmoid(2 z).
 constexpr float kGeluC = 1.5957691216057308f, kGeluA = 0.044715f;
 
+// Phi(x), the normal distribution function, and e = exp(-x^2 / 2). With t = 1 / (1 + p z), z = |x| /
+// sqrt 2: erfc(z) = (a1 t + ... + a5 t^5) exp(-z^2) + d, |d| <= 1.5e-7 (Abramowitz and Stegun,
+// Handbook of Mathematical Functions, 7.1.26), so Phi is within 2^-23 and x Phi(x) within
+// 2^-23 |x|, with no 1 + erf to cancel for x < 0. One exponential and one division; CUDA's erff
+// took 146 us where this takes the epilogue of 8192 x 6144 x 2048 (bias, GELU) %GELU% us.
+__device__ __forceinline__ float normal_cdf(float x, float& e)
+{
+    e = expf(-0.5f * x * x);
+    const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(x), 1.0f));
+    float q = fmaf(t, 1.061405429f, -1.453152027f);
+    q = fmaf(t, q, 1.421413741f);
+    q = fmaf(t, q, -0.284496736f);
+    q = fmaf(t, q, 0.254829592f);
+    q = 0.5f * q * t * e;
+    return x < 0.0f ? q : 1.0f - q;
+}
+
 // v = act(v) for all elements (the switch is uniform, one branch per array).
 template <int N>
 __device__ __forceinline__ void act_apply(float (&v)[N], int32_t act)
@@ -47,7 +64,10 @@ __device__ __forceinline__ void act_apply(float (&v)[N], int32_t act)
             break;
         case kActGelu:
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
+            for (int i = 0; i < N; ++i) {
+                float e;
+                v[i] *= normal_cdf(v[i], e);
+            }
             break;
         case kActGeluTanh:
 #pragma unroll
@@ -78,9 +98,9 @@ __device__ __forceinline__ void act_apply_grad(float (&v)[N], float (&d)[N], int
             // Phi(x) + x phi(x)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float x = v[i];
-                const float cdf = 0.5f * (1.0f + erff(x * 0.70710678118654752f));
-                d[i] = fmaf(x, 0.3989422804014327f * expf(-0.5f * x * x), cdf);
+                float e;
+                const float x = v[i], cdf = normal_cdf(x, e);
+                d[i] = fmaf(x * e, 0.3989422804014327f, cdf);
                 v[i] = x * cdf;
             }
             break;
@@ -163,99 +183,6 @@ __device__ __forceinline__ void store_out4(const GemmArgs& a, size_t idx, const 
             make_uint2(pack_out16x2(v[0], v[1], a.out_dtype), pack_out16x2(v[2], v[3], a.out_dtype));
 }
 
-// A 4 x 4 transpose of 16-byte chunks within each group of 4 lanes (transpose_chunks8 for rows of
-// 64 bytes): lane 4 g + j leaves with chunk j of rows 4 g .. 4 g + 3. Its own inverse.
-__device__ __forceinline__ void transpose_chunks4(uint32_t (&w)[4][4], int lane)
-{
-    const int j = lane & 3;
-#pragma unroll
-    for (int m = 2; m >= 1; m >>= 1) {
-        const bool hi = (j & m) != 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (e & m) continue;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t send = hi ? w[e][k] : w[e ^ m][k];
-                const uint32_t recv = __shfl_xor_sync(0xffffffffu, send, m);
-                if (hi) w[e][k] = recv;
-                else w[e ^ m][k] = recv;
-            }
-        }
-    }
-}
-
-// 32 consecutive elements (columns col .. col + 31 of a row-major array with row stride ld) of
-// each of the warp's 32 rows row0 + lane, one row per lane in registers, moved as 64-byte
-// (16-bit types) or 128-byte (fp32) row segments: a transpose among 4 or 8 lanes turns each
-// lane's row into the chunk it loads or stores of 4 or 8 rows. Rows from M and columns from
-// n_end (a multiple of 8) on are not touched; they load as 0.
-__device__ __forceinline__ void load_rows32(const void* src, int32_t dt, int64_t ld, int row0, int M, int col,
-                                            int n_end, int lane, float (&v)[32])
-{
-    if (dt == kOutF32) {
-        const int n = col + 4 * (lane & 7);
-        uint32_t w[8][4];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const int m = row0 + (lane & ~7) + t;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (m < M && n < n_end) x = *reinterpret_cast<const uint4*>(static_cast<const float*>(src) + m * ld + n);
-            w[t][0] = x.x; w[t][1] = x.y; w[t][2] = x.z; w[t][3] = x.w;
-        }
-        transpose_chunks8(w, lane);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i >> 2][i & 3]);
-    } else {
-        const int n = col + 8 * (lane & 3);
-        uint32_t w[4][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int m = row0 + (lane & ~3) + t;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (m < M && n < n_end) x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + m * ld + n);
-            w[t][0] = x.x; w[t][1] = x.y; w[t][2] = x.z; w[t][3] = x.w;
-        }
-        transpose_chunks4(w, lane);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 f = unpack_out16x2(w[i >> 2][i & 3], dt);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
-    }
-}
-
-__device__ __forceinline__ void store_rows32(void* dst, int32_t dt, int64_t ld, int row0, int M, int col, int lane,
-                                             const float (&v)[32])
-{
-    if (dt == kOutF32) {
-        uint32_t w[8][4];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) w[i >> 2][i & 3] = __float_as_uint(v[i]);
-        transpose_chunks8(w, lane);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const int m = row0 + (lane & ~7) + t;
-            if (m < M)
-                *reinterpret_cast<uint4*>(static_cast<float*>(dst) + m * ld + col + 4 * (lane & 7)) =
-                    make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
-        }
-    } else {
-        uint32_t w[4][4];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = pack_out16x2(v[2 * i], v[2 * i + 1], dt);
-        transpose_chunks4(w, lane);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int m = row0 + (lane & ~3) + t;
-            if (m < M)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + m * ld + col + 8 * (lane & 3)) =
-                    make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
-        }
-    }
-}
-
 // ------------------------------------------------------------------ NVFP4 output of h
 
 // Where the scale of block `blk` (16 elements) of row `row` of h goes.
@@ -278,16 +205,14 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float gs, float& r)
 
 // ------------------------------------------------------------------ bias, activation, residual
 
-// v = act(alpha * acc + bias) of N consecutive output columns n0 .. of one row (N a multiple of
-// 8; columns past a.N read no bias, N % 8 == 0 of the output).
+// v = act(alpha * acc + bias) of N consecutive output columns; bias: N floats (null: none).
 template <int N>
-__device__ __forceinline__ void linear_act(const GemmArgs& a, int n0, float alpha, float (&v)[N])
+__device__ __forceinline__ void linear_act(const float* bias, int32_t act, float alpha, float (&v)[N])
 {
-    if (a.bias != nullptr) {
+    if (bias != nullptr) {
 #pragma unroll
         for (int k = 0; k < N; k += 4) {
-            float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (n0 + k < a.N) b = __ldg(reinterpret_cast<const float4*>(a.bias + n0 + k));
+            const float4 b = *reinterpret_cast<const float4*>(bias + k);
             v[k] = fmaf(alpha, v[k], b.x);
             v[k + 1] = fmaf(alpha, v[k + 1], b.y);
             v[k + 2] = fmaf(alpha, v[k + 2], b.z);
@@ -297,32 +222,7 @@ __device__ __forceinline__ void linear_act(const GemmArgs& a, int n0, float alph
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] *= alpha;
     }
-    act_apply(v, a.act_fn);
-}
-
-template <class Cfg>
-__device__ __forceinline__ void linear_rows64(const GemmArgs& a, const Tile& ti, int quad, int lane, int c0,
-                                              const uint32_t (&r)[4][16], float alpha)
-{
-    const int row0 = ti.p0 + 32 * quad;
-    uint32_t o[4][16];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int n0 = ti.q0 + c0 + 32 * h;
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[2 * h + (i >> 4)][i & 15]);
-        linear_act(a, n0, alpha, v);
-        if (a.side != nullptr) {
-            float s[32];
-            load_rows32(a.side, a.out_dtype, a.N, row0, a.M, n0, a.N, lane, s);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(a.side_scale, s[i], v[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[2 * h + (i >> 4)][i & 15] = __float_as_uint(v[i]);
-    }
-    store_rows64<Cfg>(a, ti, quad, lane, c0, o, 1.0f);
+    act_apply(v, act);
 }
 
 // Swap tiles: the lane's output column n = p0 + 32 quad + lane, tokens c .. c + 15.
@@ -391,7 +291,7 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& ti, 
                 }
             }
         }
-        linear_act(a, n0, alpha, v);
+        linear_act(a.bias != nullptr ? a.bias + n0 : nullptr, a.act_fn, alpha, v);
         if (a.side != nullptr) {
 #pragma unroll
             for (int t = 0; t < 8; ++t) v[t] = fmaf(a.side_scale, s[t], v[t]);
@@ -401,61 +301,6 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& ti, 
 }
 
 // ------------------------------------------------------------------ gated product
-
-// Token-major tiles: columns c0 .. c0 + 63 are [16 gate, 16 up, 16 gate, 16 up] of 32 indices of
-// h, all in the thread of their token (I % 32 == 0: the 32 are inside I or past it together).
-template <class Cfg>
-__device__ __forceinline__ void glu_rows64(const GemmArgs& a, const Tile& ti, int quad, int lane, int c0,
-                                           const uint32_t (&r)[4][16], float alpha)
-{
-    const int j0 = (ti.q0 + c0) >> 1;
-    if (j0 >= a.inter) return;                       // warp-uniform
-    const int row0 = ti.p0 + 32 * quad;
-    float h[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) h[i] = alpha * __uint_as_float(r[2 * (i >> 4)][i & 15]);
-    if constexpr (Cfg::EPI == kEpiGluGrad) {
-        float s[32], d[32];
-        load_rows32(a.side, a.out_dtype, a.inter, row0, a.M, j0, a.inter, lane, s);
-        act_apply_grad(h, d, a.act_fn);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float u = alpha * __uint_as_float(r[2 * (i >> 4) + 1][i & 15]);
-            d[i] = s[i] * u * d[i];
-            h[i] = s[i] * h[i];
-        }
-        store_rows32(a.out, a.out_dtype, a.N, row0, a.M, j0, lane, d);
-        store_rows32(a.out, a.out_dtype, a.N, row0, a.M, a.inter + j0, lane, h);
-    } else {
-        act_apply(h, a.act_fn);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) h[i] *= alpha * __uint_as_float(r[2 * (i >> 4) + 1][i & 15]);
-        if constexpr (Cfg::EPI == kEpiGlu) {
-            store_rows32(a.out, a.out_dtype, a.inter, row0, a.M, j0, lane, h);
-        } else {
-            const float gs = __ldg(a.gs_h);
-            uint32_t q[4], sf = 0;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float amax = 0.0f, rcp, lo[8], hi[8];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(h[16 * b + i]));
-                sf |= block_scale(amax, gs, rcp) << (8 * b);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) { lo[i] = h[16 * b + i]; hi[i] = h[16 * b + 8 + i]; }
-                q[2 * b] = scale_to_e2m1x8(lo, rcp);
-                q[2 * b + 1] = scale_to_e2m1x8(hi, rcp);
-            }
-            const int m = row0 + lane;
-            if (m < a.M) {
-                // 16 bytes of codes and two neighbouring scale bytes (an even block index)
-                *reinterpret_cast<uint4*>(a.h_q + static_cast<int64_t>(m) * (a.inter >> 1) + (j0 >> 1)) =
-                    make_uint4(q[0], q[1], q[2], q[3]);
-                *reinterpret_cast<uint16_t*>(h_sf_at(a, m, j0 >> 4)) = static_cast<uint16_t>(sf);
-            }
-        }
-    }
-}
 
 // One (g, u) pair of h index j of token m, after the reduction; the 16 lanes of a half-warp hold
 // the 16 indices of one block of the same token. `ok`: the token exists. All lanes take part.
@@ -584,15 +429,349 @@ __device__ __forceinline__ void glu_chunk(const GemmArgs& a, const Tile& ti, con
     }
 }
 
-// ------------------------------------------------------------------ dispatch (gemm_kernel.cuh)
+// ------------------------------------------------------------------ token-major tiles
 
+// A warp's part of a token-major tile: 32 token rows (lane = row) x up to two chunks of 64
+// accumulator columns, taken in pieces of 32. Results leave, and the residual or dh comes in, as
+// boxes of 64 bytes x 32 rows by TMA through two buffers per warp (64-byte swizzle: a lane's four
+// 16-byte pieces of its row are conflict-free, and no lane exchanges data with another). The
+// boxes are requested before the accumulator is awaited where a buffer is free, and a result
+// takes the place of the side value it used.
+//
+// The loops over chunks and pieces are not unrolled: the epilogue's straight-line code would
+// otherwise pass the instruction cache once per tile and warp (8192 x 6144 x 2048 with bias and
+// GELU: %UNROLL%).
+//
+// Per 32-column piece: kEpiLinear one box of a 16-bit type or two of fp32; the gated ones 16
+// indices of h ([16 gate, 16 up] columns): half a box of a 16-bit type or one of fp32.
 template <class Cfg>
-__device__ __forceinline__ void epi_rows64(const GemmArgs& a, const Tile& ti, int quad, int lane, int c0,
-                                           const uint32_t (&r)[4][16], float alpha)
-{
-    if constexpr (Cfg::EPI == kEpiLinear) linear_rows64<Cfg>(a, ti, quad, lane, c0, r, alpha);
-    else glu_rows64<Cfg>(a, ti, quad, lane, c0, r, alpha);
-}
+struct EpiRows {
+    static constexpr bool LINEAR = Cfg::EPI == kEpiLinear;
+    static constexpr bool GRAD = Cfg::EPI == kEpiGluGrad;
+    static constexpr bool QUANT = Cfg::EPI == kEpiGluQuant;
+    static constexpr int BOX = Cfg::EPI_BOX;
+
+    const GemmArgs& a;
+    const EpiMaps<true>& maps;
+    const AbortState& ab;
+    uint8_t* const buf;          // two boxes
+    float* const bias_s;         // 64 floats
+    uint64_t* const bar;         // side box landed, per buffer
+    const int quad, lane, half;
+    const bool f32;
+    uint32_t phases = 0;         // bit b: parity of the next wait for buffer b
+    uint32_t pending = 0;        // bit b: a side box is on its way into buffer b
+    int turn = 0;                // kEpiGlu: the buffer of the next box (a tile can have an odd number)
+    float2 bias[2];              // of chunk 0 and 1, two columns per lane
+
+    // smem: the boxes of all epilogue warps (512-byte aligned, as their swizzle is), then their biases
+    __device__ __forceinline__ EpiRows(const GemmArgs& args, const EpiMaps<true>& m, int q, int l, int h, uint8_t* smem,
+                                       uint64_t* bars, const AbortState& abort)
+        : a(args), maps(m), ab(abort), buf(smem + (4 * h + q) * Cfg::EPI_WARP),
+          bias_s(reinterpret_cast<float*>(smem + kEpilogueWarps * Cfg::EPI_WARP + (4 * h + q) * Cfg::EPI_BIAS)),
+          bar(bars + 2 * (4 * h + q)), quad(q), lane(l), half(h), f32(args.out_dtype == kOutF32)
+    {
+    }
+
+    // Chunks of the tile in this warp's order: the last columns of the tile first for the second
+    // warpgroup (with SF_IN_ACC they hold the next tile's scales).
+    __device__ __forceinline__ int chunk_col(const Tile& ti, int k) const
+    {
+        const int cols = Cfg::NARROW ? ti.q_span : Cfg::BN;
+        return half ? cols - 64 * (k + 1) : 64 * k;
+    }
+    __device__ __forceinline__ int chunks(const Tile& ti) const { return (Cfg::NARROW ? ti.q_span : Cfg::BN) / 128; }
+
+    // Boxes of the tile are numbered in the warp's order; `first_col` is the output column (of h
+    // for the gated products) that box u starts at.
+    __device__ __forceinline__ int boxes_per_chunk() const { return LINEAR ? (f32 ? 4 : 2) : (f32 ? 2 : 1); }
+    __device__ __forceinline__ int box_cols() const { return f32 ? 16 : 32; }
+    __device__ __forceinline__ int first_col(const Tile& ti, int u) const
+    {
+        const int bpc = boxes_per_chunk(), k = u / bpc;
+        const int c = ti.q0 + chunk_col(ti, k);
+        return (LINEAR ? c : c >> 1) + (u - k * bpc) * box_cols();
+    }
+    __device__ __forceinline__ int end_col() const { return LINEAR ? a.N : a.inter; }
+
+    // Lane 0: side box u into buffer b (free). Boxes wholly past the columns are not requested.
+    __device__ __forceinline__ void request(const Tile& ti, int u, int b)
+    {
+        const int n = first_col(ti, u);
+        if (n >= end_col()) return;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bar[b], BOX);
+            tma_load_2d(buf + b * BOX, &maps.side, &bar[b], n * (f32 ? 4 : 2), ti.p0 + 32 * quad, l2_policy_evict_first());
+        }
+        pending |= 1u << b;
+    }
+    __device__ __forceinline__ bool landed(int b)
+    {
+        if (!(pending >> b & 1u)) return true;
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(&bar[b], phases >> b & 1u, ab, kErrEpiSide));
+        if (ok) {
+            phases ^= 1u << b;
+            pending &= ~(1u << b);
+        }
+        return ok;
+    }
+
+    __device__ __forceinline__ bool active(const Tile& ti) const { return ti.p0 + 32 * quad < a.M; }
+
+    __device__ __forceinline__ void begin(const Tile& ti)
+    {
+        if (!active(ti)) return;
+        if constexpr (LINEAR || GRAD) {
+            if (a.side != nullptr) {
+                if (lane == 0) bulk_wait_read<0>();
+                request(ti, 0, 0);
+                if (LINEAR) request(ti, 1, 1);       // (GRAD's second buffer takes du)
+            }
+        }
+        if constexpr (LINEAR) {
+            if (a.bias != nullptr) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int n = ti.q0 + chunk_col(ti, k) + 2 * lane;
+                    bias[k] = make_float2(0.0f, 0.0f);
+                    if (k < chunks(ti) && n < a.N) bias[k] = __ldg(reinterpret_cast<const float2*>(a.bias + n));
+                }
+            }
+        }
+    }
+
+    // The 16-byte piece e of this lane's row in buffer b.
+    __device__ __forceinline__ uint4* slot(int b, int e) const
+    {
+        return reinterpret_cast<uint4*>(buf + b * BOX + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4));
+    }
+
+    // Buffer b, written by every lane, to output column n. (A box past the columns still makes a
+    // bulk group, so that buffers_free<1> means "the other buffer" everywhere.)
+    __device__ __forceinline__ void send(const Tile& ti, int b, int n)
+    {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (n < end_col()) tma_store_2d(&maps.out, buf + b * BOX, n * (f32 ? 4 : 2), ti.p0 + 32 * quad);
+            bulk_commit();
+        }
+    }
+
+    // Lane 0 waits until all but the latest N stores have left their buffers.
+    template <int N>
+    __device__ __forceinline__ void buffers_free()
+    {
+        if (lane == 0) bulk_wait_read<N>();
+        __syncwarp();
+    }
+
+    // 16 values as output elements in pieces e0 .. of buffer b (2 pieces of a 16-bit type, 4 of fp32)
+    __device__ __forceinline__ void put16(int b, int e0, const float (&v)[16]) const
+    {
+        if (f32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *slot(b, e) = make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
+                                         __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
+        } else {
+            const int32_t dt = a.out_dtype;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *slot(b, e0 + e) = make_uint4(pack_out16x2(v[8 * e], v[8 * e + 1], dt), pack_out16x2(v[8 * e + 2], v[8 * e + 3], dt),
+                                              pack_out16x2(v[8 * e + 4], v[8 * e + 5], dt), pack_out16x2(v[8 * e + 6], v[8 * e + 7], dt));
+        }
+    }
+    __device__ __forceinline__ void get16(int b, int e0, float (&v)[16]) const
+    {
+        if (f32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint4 x = *slot(b, e);
+                v[4 * e] = __uint_as_float(x.x); v[4 * e + 1] = __uint_as_float(x.y);
+                v[4 * e + 2] = __uint_as_float(x.z); v[4 * e + 3] = __uint_as_float(x.w);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint4 x = *slot(b, e0 + e);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack_out16x2(w[i], a.out_dtype);
+                    v[8 * e + 2 * i] = f.x;
+                    v[8 * e + 2 * i + 1] = f.y;
+                }
+            }
+        }
+    }
+
+    // Piece h (32 columns, r) of chunk k.
+    __device__ __forceinline__ bool linear_piece(const Tile& ti, int k, int h, const uint32_t (&r)[32], float alpha)
+    {
+        const int total = chunks(ti) * boxes_per_chunk();
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        linear_act(a.bias != nullptr ? bias_s + 32 * h : nullptr, a.act_fn, alpha, v);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {                // the two halves of the piece: 16 columns each
+            float w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = v[16 * s + i];
+            const int u = f32 ? 4 * k + 2 * h + s : 2 * k + h;
+            const int b = u & 1, e0 = 2 * s;
+            const bool opens = f32 || s == 0, closes = f32 || s == 1;
+            if (opens) {
+                if (a.side != nullptr) {
+                    if (u >= 1 && u + 1 < total) {   // the other buffer is the next box's
+                        buffers_free<0>();
+                        request(ti, u + 1, b ^ 1);
+                    }
+                    if (!landed(b)) return false;
+                } else {
+                    buffers_free<1>();
+                }
+            }
+            if (a.side != nullptr) {
+                float x[16];
+                get16(b, e0, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = fmaf(a.side_scale, x[i], w[i]);
+            }
+            put16(b, e0, w);
+            if (closes) send(ti, b, first_col(ti, u));
+        }
+        return true;
+    }
+
+    // 16 indices of h from [16 gate, 16 up] columns.
+    __device__ __forceinline__ bool glu_piece(const Tile& ti, int k, int h, const uint32_t (&r)[32], float alpha,
+                                              uint32_t (&q)[4], uint32_t& sf)
+    {
+        const int j0 = ((ti.q0 + chunk_col(ti, k)) >> 1) + 16 * h;
+        float g[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g[i] = alpha * __uint_as_float(r[i]);
+        if constexpr (GRAD) {
+            const int u = f32 ? 2 * k + h : k, e0 = 2 * h;
+            if ((f32 || h == 0) && u > 0) {
+                buffers_free<0>();
+                request(ti, u, 0);
+            }
+            if (!landed(0)) return false;
+            float d[16], x[16];
+            act_apply_grad(g, d, a.act_fn);
+            get16(0, e0, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                d[i] *= alpha * __uint_as_float(r[16 + i]) * x[i];
+                g[i] *= x[i];
+            }
+            put16(0, e0, d);
+            put16(1, e0, g);
+            if (f32 || h == 1) {
+                const int n = first_col(ti, u);
+                if (n < a.inter) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int esz = f32 ? 4 : 2;
+                        tma_store_2d(&maps.out, buf, n * esz, ti.p0 + 32 * quad);
+                        tma_store_2d(&maps.out, buf + BOX, (a.inter + n) * esz, ti.p0 + 32 * quad);
+                        bulk_commit();
+                    }
+                }
+            }
+            return true;
+        }
+        act_apply(g, a.act_fn);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g[i] *= alpha * __uint_as_float(r[16 + i]);
+        if constexpr (QUANT) {
+            // one NVFP4 block per piece; a row's two blocks of a chunk leave together
+            float amax = 0.0f, rcp, lo[8], hi[8];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(g[i]));
+            const uint32_t s = block_scale(amax, __ldg(a.gs_h), rcp);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) { lo[i] = g[i]; hi[i] = g[8 + i]; }
+            q[2] = scale_to_e2m1x8(lo, rcp);
+            q[3] = scale_to_e2m1x8(hi, rcp);
+            if (h == 0) {
+                q[0] = q[2];
+                q[1] = q[3];
+                sf = s;
+            } else {
+                const int m = ti.p0 + 32 * quad + lane;
+                if (m < a.M && j0 < a.inter) {
+                    *reinterpret_cast<uint4*>(a.h_q + static_cast<int64_t>(m) * (a.inter >> 1) + ((j0 - 16) >> 1)) =
+                        make_uint4(q[0], q[1], q[2], q[3]);
+                    *reinterpret_cast<uint16_t*>(h_sf_at(a, m, (j0 >> 4) - 1)) = static_cast<uint16_t>(sf | s << 8);
+                }
+            }
+        } else {
+            if (f32 || h == 0) buffers_free<1>();
+            put16(turn, 2 * h, g);
+            if (f32 || h == 1) {
+                send(ti, turn, first_col(ti, f32 ? 2 * k + h : k));
+                turn ^= 1;
+            }
+        }
+        return true;
+    }
+
+    // Drains the tile from TMEM (tacc: this warp's lanes and the accumulator's first column);
+    // `drained` is called once the first chunk is in registers.
+    template <class F>
+    __device__ __forceinline__ bool finish(const Tile& ti, uint32_t tacc, float alpha, F drained)
+    {
+        if (!active(ti)) {
+            drained();
+            return true;
+        }
+        uint32_t q[4], sf = 0;
+        bool ok = true;
+        const int nk = chunks(ti);
+#pragma unroll 1
+        for (int k = 0; k < nk; ++k) {
+            uint32_t r[4][16], cur[32];
+            const uint32_t t0 = tacc + chunk_col(ti, k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x16(t0 + 16 * i, r[i]);
+            if constexpr (LINEAR) {
+                if (a.bias != nullptr) {
+                    __syncwarp();                    // the chunk before has read its bias
+                    reinterpret_cast<float2*>(bias_s)[lane] = k == 0 ? bias[0] : bias[1];
+                    __syncwarp();
+                }
+            }
+            tmem_ld_wait();
+            if (k == 0) drained();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) cur[i] = r[i >> 4][i & 15];
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (LINEAR) ok = ok && linear_piece(ti, k, h, cur, alpha);
+                else ok = ok && glu_piece(ti, k, h, cur, alpha, q, sf);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) cur[i] = r[2 + (i >> 4)][i & 15];
+            }
+        }
+        return __all_sync(0xffffffffu, ok);
+    }
+
+    // Before the CTA's shared memory is released: every box has landed and every store has read.
+    __device__ __forceinline__ void drain()
+    {
+        for (int b = 0; b < 2; ++b)
+            if (pending >> b & 1u) mbar_wait_drain(&bar[b], phases >> b & 1u);
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+    }
+};
+
+// ------------------------------------------------------------------ dispatch (gemm_kernel.cuh)
 
 template <class Cfg>
 __device__ __forceinline__ void epi_tok16(const GemmArgs& a, const Tile& ti, int quad, int lane, int c,

@@ -34,6 +34,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,6 +57,7 @@ enum : uint32_t {
     kErrMmaSfFree = 0x108,
     kErrActqMax = 0x10B,
     kErrMmaActq = 0x10C,
+    kErrEpiSide = 0x10D,
 };
 
 // Threads per CTA: warps 0-3 (producer, MMA, scale re-layout) and two epilogue warpgroups.
@@ -106,6 +108,16 @@ struct GemmArgs {
     const void* side;         // kEpiLinear: residual [M][N] or null; kEpiGluGrad: dh [M][I]; out_dtype elements
     float side_scale;         // kEpiLinear: residual_scale
     int32_t h_sf_tiled;       // kEpiGluQuant: h_sf in the tiled layout (1) or row-major (0)
+};
+
+// Tensor maps of a fused epilogue's output and side input (residual, dh): rows of elements, boxes
+// of 64 bytes x 32 rows. An empty parameter elsewhere.
+template <bool ON>
+struct EpiMaps {
+};
+template <>
+struct EpiMaps<true> {
+    CUtensorMap out, side;
 };
 
 template <int BN_, bool SWAP_, bool GROUPED_, bool SFT_ = false, bool SWIGLU_ = false, bool MX_ = false,
@@ -166,8 +178,10 @@ struct GemmCfg {
     // the (g, u) pairs of one 16-element block of h; its tiled scales are stored in that order.
     static constexpr int EPI = EPI_;
     static constexpr bool GLU = EPI >= kEpiGlu;
-    static_assert(EPI == kEpiPlain || (SFT && !GROUPED && !MX && !ACTQ && !(PAIR && BN != 256)),
-                  "fused epilogues serve the dense NVFP4 product with tiled scales");
+    static_assert(EPI == kEpiPlain || (SFT && !GROUPED && !MX && !ACTQ && (SWAP || BN == (PAIR ? 256 : 128))),
+                  "fused epilogues serve the dense NVFP4 product with tiled scales: few-token tiles, "
+                  "128-wide tiles and 256-wide CTA pairs");
+    static constexpr bool EPI_ROWS = EPI != kEpiPlain && !SWAP;   // token-major fused tiles
     static constexpr int ACTQ_BYTES = ACTQ ? 1024 + 64 + 64 : 0;   // gs / e4m3 table, maxima slots, reduction
     static_assert(!SFT || BN % 128 == 0 || (SWAP && BN <= 64), "Q tiles on 128-row tile boundaries");
     static_assert(!GROUPED || SWAP, "grouped GEMM runs with weights as the MMA M operand");
@@ -228,8 +242,15 @@ struct GemmCfg {
     static constexpr int CHUNK_ROWS = GLU && SWAP ? 32 : 8;   // rows that stay together
     static constexpr int RX_ROWS = CHUNK_ROWS == 32 ? 256 : 168;
     static constexpr int RX_BYTES = RX_OWN ? ((RX_ROWS * PSTRIDE * 4 + 1023) & ~1023) : 0;
+    // EPI_ROWS: per epilogue warp two 2 KB boxes (side input in, results out) and the bias of a
+    // 64-column chunk. Costs 128-wide tiles one of their six ring stages; CTA pairs keep all five
+    // (a fourth KB per warp would cost them one: 5-11% of 8192 x 6144 x 2048 and larger).
+    static constexpr int EPI_BOX = 2048;
+    static constexpr int EPI_WARP = 2 * EPI_BOX;
+    static constexpr int EPI_BIAS = EPI == kEpiLinear ? 256 : 0;
+    static constexpr int EPI_BYTES = EPI_ROWS ? kEpilogueWarps * (EPI_WARP + EPI_BIAS) : 0;
     static constexpr int MISC_BYTES = 1024 + (GROUPED ? 4 * (kMaxExperts + 1) : 0) + SWIGLU_BYTES + RX_BYTES +
-                                      ACTQ_BYTES;
+                                      ACTQ_BYTES + EPI_BYTES;
     static constexpr int ALIGN_SLACK = 1024;
     static constexpr int STAGES_FIT = (SMEM_LIMIT - MISC_BYTES - ALIGN_SLACK) / STAGE_BYTES;
     // Few-token (swap, non-grouped) launches split K finely and run a handful of stages per
@@ -247,15 +268,17 @@ struct GemmCfg {
     // barriers: full, sfready, empty [STAGES]; acc_full, acc_empty [2]; mma_done; split-K rx;
     // sf_free [2]; activations quantised, slice maxima received (ACTQ); GPAIR: this CTA's
     // scales landed [STAGES]
-    static constexpr int NUM_BARS = 4 * STAGES + 10;
+    // EPI_ROWS: side input landed, two per epilogue warp
+    static constexpr int NUM_BARS = 4 * STAGES + 10 + (EPI_ROWS ? 2 * kEpilogueWarps : 0);
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;     // tmem base, flags
     static constexpr int OFF_PREFIX = OFF_MISC + 64;
     static constexpr int OFF_SWIGLU = OFF_PREFIX + (GROUPED ? ((4 * (kMaxExperts + 1) + 15) & ~15) : 0);
     static constexpr int OFF_RX = (OFF_SWIGLU + SWIGLU_BYTES + 1023) & ~1023;
     static constexpr int OFF_ACTQ = OFF_RX + RX_BYTES;
-    static constexpr int SMEM_BYTES = OFF_ACTQ + ACTQ_BYTES + ALIGN_SLACK;
+    static constexpr int OFF_EPI = (OFF_ACTQ + ACTQ_BYTES + 1023) & ~1023;
+    static constexpr int SMEM_BYTES = OFF_EPI + EPI_BYTES + ALIGN_SLACK;
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
-    static_assert(RX_OWN || RX_ROWS * PSTRIDE * 4 <= STAGES * STAGE_BYTES, "split-K receive buffer fits the pipeline buffers");
+    static_assert(RX_OWN || PAIR || RX_ROWS * PSTRIDE * 4 <= STAGES * STAGE_BYTES, "split-K receive buffer fits the pipeline buffers");
     static_assert(OFF_Q % 1024 == 0 && OFF_SFP % 1024 == 0, "swizzle atoms need 1 KB alignment");
 };
 
@@ -845,12 +868,15 @@ __device__ __forceinline__ float actq_quantize_t(const GemmArgs& a, uint8_t* sme
 }
 
 // The fused epilogues (EPI), defined in gemm_epilogue.cuh, which every translation unit that
-// instantiates them includes. epi_rows64: 64 accumulator columns c0 .. c0 + 63 of a warp's 32 rows
-// (non-swap tiles, lane = token row); epi_tok16: 16 columns (tokens) of a warp's 32 weight rows
-// (swap tiles); epi_chunk: a reduced split-K chunk, in the terms of store_chunk.
+// instantiates them includes. EpiRows: a warp's part of a non-swap tile (begin() requests what the
+// tile reads besides the accumulator, finish() drains it); epi_tok16: 16 columns (tokens) of a
+// warp's 32 weight rows (swap tiles); epi_chunk: a reduced split-K chunk, in the terms of
+// store_chunk.
 template <class Cfg>
-__device__ __forceinline__ void epi_rows64(const GemmArgs& a, const Tile& ti, int quad, int lane, int c0,
-                                           const uint32_t (&r)[4][16], float alpha);
+struct EpiRows;
+struct NoEpiRows {
+    __device__ NoEpiRows(const GemmArgs&, const EpiMaps<false>&, int, int, int, uint8_t*, uint64_t*, const AbortState&) {}
+};
 template <class Cfg>
 __device__ __forceinline__ void epi_tok16(const GemmArgs& a, const Tile& ti, int quad, int lane, int c,
                                           const uint32_t (&r)[16], float alpha);
@@ -1034,7 +1060,8 @@ template <class Cfg>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_sfp, const __grid_constant__ CUtensorMap tm_sfq,
-                  const __grid_constant__ CUtensorMap tm_q_half, const GemmArgs args)
+                  const __grid_constant__ CUtensorMap tm_q_half, const GemmArgs args,
+                  const __grid_constant__ EpiMaps<Cfg::EPI_ROWS> tm_epi)
 {
     constexpr int BN = Cfg::BN;
     constexpr int STAGES = Cfg::STAGES;
@@ -1056,6 +1083,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
     uint64_t* actq_bar = bars + 3 * STAGES + 8;     // ACTQ: the Q stages hold the activations
     uint64_t* amax_bar = bars + 3 * STAGES + 9;     // ACTQ: the peers' slice maxima arrived
     uint64_t* sf_full_bar = bars + 3 * STAGES + 10; // GPAIR: this CTA's scales of stage s landed
+    uint64_t* side_bar = bars + 4 * STAGES + 10;    // EPI_ROWS: side input boxes landed, two per warp
     uint32_t* s_tmem_base = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
     volatile int* s_is_last = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 8);
@@ -1079,6 +1107,9 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             // PAIR: the even CTA's barriers count both CTAs' epilogue warps
             mbar_init(&acc_empty_bar[s], Cfg::PAIR ? 2 * kEpilogueWarps : kEpilogueWarps);
             mbar_init(&sf_free_bar[s], Cfg::PAIR ? 8 : 4);   // the second epilogue warpgroup(s)
+        }
+        if constexpr (Cfg::EPI_ROWS) {
+            for (int s = 0; s < 2 * kEpilogueWarps; ++s) mbar_init(&side_bar[s], 1);
         }
         mbar_init(mma_done_bar, 1);
         mbar_init(rx_bar, 1);
@@ -1537,9 +1568,14 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             rcp_tab[code] = (sfd == 0.0f) ? 0.0f : __fdiv_rn(gsh, sfd);
             named_bar_sync(1, 32 * kEpilogueWarps);
         }
+        std::conditional_t<Cfg::EPI_ROWS, EpiRows<Cfg>, NoEpiRows> epi(
+            args, tm_epi, quad, lane, half, smem + Cfg::OFF_EPI, side_bar, ab);
         uint32_t acc = 0, acc_phase = 0;
         for (int32_t t = tile_start; t < num_tiles; t += tile_step) {
             const Tile ti = decode_tile<Cfg>(args, t, s_prefix);
+            if constexpr (Cfg::EPI_ROWS) {
+                if (args.splits == 1) epi.begin(ti);
+            }
             bool ok = mbar_wait(&acc_full_bar[acc], acc_phase, ab, kErrEpiAccFull);
             ok = named_bar_and(1, 32 * kEpilogueWarps, ok);
             if (!ok) {
@@ -1571,7 +1607,22 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             const int mid = ((n_cols / 2 + 15) / 16) * 16;
             const int c_lo = half ? mid : 0;
             int c_hi = split_k ? c_lo : (half ? n_cols : mid);
-            if constexpr (Cfg::SF_IN_ACC) {
+            if constexpr (Cfg::EPI_ROWS) {
+                if (!split_k) {
+                    // (the second warpgroup's first chunk holds the next tile's scale columns: handed
+                    // back as soon as it is in registers)
+                    ok = epi.finish(ti, tacc, alpha, [&] {
+                        if (Cfg::SF_IN_ACC && half == 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if constexpr (Cfg::PAIR) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&sf_free_bar[acc]), 0));
+                                else mbar_arrive_relaxed(&sf_free_bar[acc]);
+                            }
+                        }
+                    });
+                }
+            } else if constexpr (Cfg::SF_IN_ACC) {
                 // the second warpgroup frees the last 64 columns (the next tile's scale
                 // columns) first: into registers, signal, then store them
                 if (half == 1 && !split_k) {
@@ -1589,9 +1640,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
                         else mbar_arrive_relaxed(&sf_free_bar[acc]);
                     }
                     if (need) {
-                        if constexpr (Cfg::EPI != kEpiPlain) {
-                            epi_rows64<Cfg>(args, ti, quad, lane, BN - 64, r, alpha);
-                        } else if constexpr (!Cfg::SWAP && !Cfg::GROUPED) {
+                        if constexpr (!Cfg::SWAP && !Cfg::GROUPED) {
                             store_rows64<Cfg>(args, ti, quad, lane, BN - 64, r, alpha);
                         } else if constexpr (Cfg::SWIGLU) {
 #pragma unroll
@@ -1614,7 +1663,9 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
                 }
             }
 
-            if constexpr (!Cfg::SWAP && !Cfg::GROUPED) {
+            if constexpr (Cfg::EPI_ROWS) {
+                // done above
+            } else if constexpr (!Cfg::SWAP && !Cfg::GROUPED) {
                 // 64-column chunks: four 16-column TMEM loads in flight, coalesced row stores
                 int c0 = c_lo;
                 for (; c0 + 64 <= c_hi; c0 += 64) {
@@ -1622,12 +1673,10 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x16(tacc + c0 + 16 * i, r[i]);
                     tmem_ld_wait();
-                    if constexpr (Cfg::EPI != kEpiPlain) epi_rows64<Cfg>(args, ti, quad, lane, c0, r, alpha);
-                    else store_rows64<Cfg>(args, ti, quad, lane, c0, r, alpha);
+                    store_rows64<Cfg>(args, ti, quad, lane, c0, r, alpha);
                 }
                 // the rest (BN = 224, 192: 48, 32 columns per half) the plain way
-                static_assert(Cfg::EPI == kEpiPlain || BN % 128 == 0, "fused epilogues take whole 64-column chunks");
-                for (; Cfg::EPI == kEpiPlain && c0 < c_hi; c0 += 16) {
+                for (; c0 < c_hi; c0 += 16) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(tacc + c0, r);
                     tmem_ld_wait();
@@ -1667,6 +1716,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             if (++acc == Cfg::ACC_STAGES) { acc = 0; acc_phase ^= 1u; }
 
         }
+        if constexpr (Cfg::EPI_ROWS) epi.drain();
     }
 
     // ------------------------------------------------------------------ teardown

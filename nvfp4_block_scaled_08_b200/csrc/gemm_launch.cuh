@@ -24,7 +24,10 @@ int max_active_clusters(int cs);
 // gemm.cu: uint8 tensor of `rank` (2 ... 5) dims (innermost first: dims[0] bytes per row), strides of
 // dims 1 .. rank-1 in bytes, box extents per dim; cached per (pointer, geometry, device).
 bool get_map_nd(CUtensorMap* out, const void* ptr, int rank, const uint64_t* dims,
-                const uint64_t* strides, const uint32_t* box, bool swizzle128);
+                const uint64_t* strides, const uint32_t* box, int swizzle);
+
+// Shared-memory swizzles of a tensor map's box.
+enum : int { kSwizzleNone = 0, kSwizzle128 = 1, kSwizzle64 = 2 };
 
 // uint8 tensor of `rank` (2 or 3) dims {inner bytes, rows[, depth]} with row stride
 // `stride1` and depth stride `stride2` (bytes); box {box0, box1[, 1]}.
@@ -35,7 +38,7 @@ inline bool get_map(CUtensorMap* out, const void* ptr, int rank, uint64_t d0, ui
     const uint64_t dims[3] = {d0, d1, d2};
     const uint64_t strides[2] = {stride1, stride2};
     const uint32_t box[3] = {box0, box1, 1};
-    return get_map_nd(out, ptr, rank, dims, strides, box, swizzle128);
+    return get_map_nd(out, ptr, rank, dims, strides, box, swizzle128 ? kSwizzle128 : kSwizzleNone);
 }
 
 // The gate_up weights [E, 2I, row_bytes] viewed so that one box of 128 rows holds four groups of
@@ -48,7 +51,7 @@ inline bool get_map_swiglu(CUtensorMap* out, const void* ptr, uint64_t row_bytes
     const uint64_t dims[5] = {row_bytes, 16, 2, I / 16, E};
     const uint64_t strides[4] = {row_bytes, I * row_bytes, 16 * row_bytes, 2 * I * row_bytes};
     const uint32_t box[5] = {box0, 16, 2, groups, 1};
-    return get_map_nd(out, ptr, 5, dims, strides, box, swizzle128);
+    return get_map_nd(out, ptr, 5, dims, strides, box, swizzle128 ? kSwizzle128 : kSwizzleNone);
 }
 
 template <int BN, bool SWAP, bool GROUPED, bool SFT = false, bool SWIGLU = false, bool MX = false,
@@ -75,6 +78,8 @@ static cudaError_t run(const GemmPlan& plan, const GemmLaunch& L, cudaStream_t s
     const uint64_t kb = static_cast<uint64_t>(L.K / 2);    // packed bytes per row
     const uint64_t ks = static_cast<uint64_t>(L.K / 16);   // scale bytes per row
     CUtensorMap tp, tq, tsp, tsq, tq_half;
+    EpiMaps<Cfg::EPI_ROWS> em;
+    std::memset(&em, 0, sizeof(em));
     bool ok = true;
     GemmArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -132,6 +137,17 @@ static cudaError_t run(const GemmPlan& plan, const GemmLaunch& L, cudaStream_t s
         // PAIR, BN = 256: each CTA's 64 rows of a 256 x 128 half tile
         if constexpr (Cfg::NARROW && GLU_Q) ok &= get_map_swiglu(&tq_half, Q, kb, I, 1, 128, true, BN / 4 / 32);
         else if constexpr (Cfg::NARROW) ok &= get_map(&tq_half, Q, 2, kb, q_rows, 1, kb, 0, 128, BN / 4, true);
+        if constexpr (Cfg::EPI_ROWS && EPI != kEpiGluQuant) {
+            // the output and the side input in boxes of 64 bytes x 32 rows
+            const uint64_t esz = L.out_dtype == kOutF32 ? 4 : 2;
+            const uint64_t out_cols = EPI == kEpiGlu ? I : static_cast<uint64_t>(L.N);
+            const uint64_t side_cols = EPI == kEpiGluGrad ? I : static_cast<uint64_t>(L.N);
+            const uint32_t box[2] = {64, 32};
+            const uint64_t od[2] = {out_cols * esz, static_cast<uint64_t>(L.M)};
+            const uint64_t sd[2] = {side_cols * esz, static_cast<uint64_t>(L.M)};
+            ok &= get_map_nd(&em.out, L.out, 2, od, od, box, kSwizzle64);
+            if (L.side) ok &= get_map_nd(&em.side, L.side, 2, sd, sd, box, kSwizzle64);
+        }
         if constexpr (EPI != kEpiPlain) {
             a.act_fn = L.act_fn;
             a.bias = L.bias;
@@ -219,7 +235,7 @@ static cudaError_t run(const GemmPlan& plan, const GemmLaunch& L, cudaStream_t s
     if constexpr (PAIR) attrs[1].val.clusterDim.x = 2;
     cfg.attrs = attrs;
     cfg.numAttrs = (PAIR || (!GROUPED && plan.cluster > 1)) ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, tp, tq, tsp, tsq, tq_half, a);
+    return cudaLaunchKernelEx(&cfg, kern, tp, tq, tsp, tsq, tq_half, a, em);
 }
 
 }  // namespace nvfp4

@@ -95,6 +95,8 @@ struct GemmPlan {
 // allow_workspace: a split-K workspace may be used (groups > 1); cluster-only split-K
 // needs none.
 GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool allow_workspace, int num_sms);
+// The tiling of a product with a fused epilogue (launch_gemm_fused).
+GemmPlan plan_fused(int64_t M, int64_t N, int64_t K, int num_sms);
 GemmPlan plan_grouped(int32_t E, int64_t total_rows, int64_t N, int64_t K, int num_sms);
 // Forces planner choices for later calls (0 = the planner's own); nvfp4_set_plan_override.
 void set_plan_override(int bn, int cluster, int groups, int band, int grouped_bn, int pair);

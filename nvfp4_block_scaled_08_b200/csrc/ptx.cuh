@@ -190,6 +190,24 @@ __device__ __forceinline__ void tma_prefetch_5d(const CUtensorMap* map, int32_t 
                  : "memory");
 }
 
+// 2-D tile store from shared memory, in this thread's current bulk group. Rows and columns past
+// the tensor are not written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+// Until all but the latest N of this thread's bulk groups have read their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 // Make this thread's generic-proxy shared-memory writes visible to the async proxy
 // (tcgen05.cp / tcgen05.mma / TMA read shared memory through the async proxy).
 __device__ __forceinline__ void fence_proxy_async_smem()
