@@ -16,43 +16,69 @@ namespace nvfp4 {
 // Activations (include/nvfp4.h, nvfp4_act).
 enum : int32_t { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4, kActRelu2 = 5 };
 
-// 1 / (1 + exp(-x)); exp overflows to infinity for x < -88.7, where the quotient is 0.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
+// The special function unit takes 8 cycles per warp and operation where the others take one, so
+// the activations below spend it on one exponential per element and one reciprocal per two:
+// 1 / d0 = d1 (1 / (d0 d1)). Arrays come in pairs (N even; a pair's NaN or infinity stays in its
+// own element). 8192 x 6144 x 2048 with SiLU / GELU / GELU_TANH: %ACT%.
 
-// p = sigmoid(x) and q = 1 - p = p exp(-x), each to a few ulp (1 - p itself would lose q where p is
-// near 1). The exponent is capped, where p is already negligible, so that exp stays finite.
-__device__ __forceinline__ void sigmoid_both(float x, float& p, float& q)
+__device__ __forceinline__ float exp2_approx(float x)          // 2^-22 relative, subnormal results 0
 {
-    const float e = expf(fminf(-x, 80.0f));
-    p = __fdividef(1.0f, 1.0f + e);
-    q = p * e;
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// 2 sqrt(2 / pi) (x + 0.044715 x^3): gelu_tanh(x) = x sigmoid(this), since
-// (1 + tanh z) / 2 = sigmoid(2 z).
-constexpr float kGeluC = 1.5957691216057308f, kGeluA = 0.044715f;
-
-// Phi(x), the normal distribution function, and e = exp(-x^2 / 2). With t = 1 / (1 + p z), z = |x| /
-// sqrt 2: erfc(z) = (a1 t + ... + a5 t^5) exp(-z^2) + d, |d| <= 1.5e-7 (Abramowitz and Stegun,
-// Handbook of Mathematical Functions, 7.1.26), so Phi is within 2^-23 and x Phi(x) within
-// 2^-23 |x|, with no 1 + erf to cancel for x < 0. One exponential and one division; CUDA's erff
-// took 146 us where this takes the epilogue of 8192 x 6144 x 2048 (bias, GELU) %GELU% us.
-__device__ __forceinline__ float normal_cdf(float x, float& e)
+// t = 1 / d of two values of 1 .. 2^61
+__device__ __forceinline__ void reciprocals(float d0, float d1, float& t0, float& t1)
 {
-    e = expf(-0.5f * x * x);
-    const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(x), 1.0f));
-    float q = fmaf(t, 1.061405429f, -1.453152027f);
-    q = fmaf(t, q, 1.421413741f);
-    q = fmaf(t, q, -0.284496736f);
-    q = fmaf(t, q, 0.254829592f);
-    q = 0.5f * q * t * e;
-    return x < 0.0f ? q : 1.0f - q;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d0 * d1));
+    t0 = r * d1;
+    t1 = r * d0;
+}
+
+// p = sigmoid(x) = 1 / (1 + e) of two values, with e = exp(-x). e is capped at 2^60, where p is
+// negligible; 1 - p is p e (1 - p itself would lose it where p is near 1).
+__device__ __forceinline__ void sigmoids(float x0, float x1, float& p0, float& p1, float& e0, float& e1)
+{
+    constexpr float kLog2e = 1.4426950408889634f;
+    e0 = exp2_approx(fminf(-kLog2e * x0, 60.0f));
+    e1 = exp2_approx(fminf(-kLog2e * x1, 60.0f));
+    reciprocals(1.0f + e0, 1.0f + e1, p0, p1);
+}
+
+// gelu_tanh(x) = x sigmoid(C x (1 + A x^2)), since (1 + tanh z) / 2 = sigmoid(2 z)
+constexpr float kGeluC = 1.5957691216057308f, kGeluA = 0.044715f;   // C = 2 sqrt(2 / pi)
+__device__ __forceinline__ float gelu_tanh_arg(float x) { return kGeluC * x * fmaf(kGeluA * x, x, 1.0f); }
+
+// Q(z) = 1 - Phi(z), Phi the normal distribution function, of z = min(|x|, 10^4), and e =
+// exp(-x^2 / 2), for two values. With t = 1 / (1 + p w), w = z / sqrt 2: erfc(w) = (a1 t + ... +
+// a5 t^5) exp(-w^2) + d, |d| <= 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26): Q is within 2^-23, with no 1 - erf to cancel.
+__device__ __forceinline__ void normal_tails(float x0, float x1, float z0, float z1, float& q0, float& q1, float& e0,
+                                             float& e1)
+{
+    constexpr float kHalfLog2e = 0.72134752044448170f, kP = 0.3275911f * 0.70710678118654752f;
+    e0 = exp2_approx(-kHalfLog2e * x0 * x0);
+    e1 = exp2_approx(-kHalfLog2e * x1 * x1);
+    float t[2], q[2];
+    reciprocals(fmaf(kP, z0, 1.0f), fmaf(kP, z1, 1.0f), t[0], t[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {       // (the coefficients halved)
+        q[i] = fmaf(t[i], 0.5307027145f, -0.7265760135f);
+        q[i] = fmaf(t[i], q[i], 0.7107068705f);
+        q[i] = fmaf(t[i], q[i], -0.142248368f);
+        q[i] = fmaf(t[i], q[i], 0.127414796f) * t[i];
+    }
+    q0 = q[0] * e0;
+    q1 = q[1] * e1;
 }
 
 // v = act(v) for all elements (the switch is uniform, one branch per array).
 template <int N>
 __device__ __forceinline__ void act_apply(float (&v)[N], int32_t act)
 {
+    static_assert(N % 2 == 0, "pairs");
     switch (act) {
         case kActRelu:
 #pragma unroll
@@ -63,19 +89,33 @@ __device__ __forceinline__ void act_apply(float (&v)[N], int32_t act)
             for (int i = 0; i < N; ++i) { const float p = v[i] < 0.0f ? 0.0f : v[i]; v[i] = p * p; }
             break;
         case kActGelu:
+            // x Phi(x) = max(x, 0) - |x| Q(|x|)
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float e;
-                v[i] *= normal_cdf(v[i], e);
+            for (int i = 0; i < N; i += 2) {
+                float q[2], e[2];
+                const float z[2] = {fminf(fabsf(v[i]), 1e4f), fminf(fabsf(v[i + 1]), 1e4f)};
+                normal_tails(v[i], v[i + 1], z[0], z[1], q[0], q[1], e[0], e[1]);
+                v[i] = fmaf(-z[0], q[0], fmaxf(v[i], 0.0f));
+                v[i + 1] = fmaf(-z[1], q[1], fmaxf(v[i + 1], 0.0f));
             }
             break;
         case kActGeluTanh:
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] *= sigmoid(kGeluC * v[i] * fmaf(kGeluA * v[i], v[i], 1.0f));
+            for (int i = 0; i < N; i += 2) {
+                float p[2], e[2];
+                sigmoids(gelu_tanh_arg(v[i]), gelu_tanh_arg(v[i + 1]), p[0], p[1], e[0], e[1]);
+                v[i] *= p[0];
+                v[i + 1] *= p[1];
+            }
             break;
         case kActSilu:
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] *= sigmoid(v[i]);
+            for (int i = 0; i < N; i += 2) {
+                float p[2], e[2];
+                sigmoids(v[i], v[i + 1], p[0], p[1], e[0], e[1]);
+                v[i] *= p[0];
+                v[i + 1] *= p[1];
+            }
             break;
         default: break;
     }
@@ -85,6 +125,7 @@ __device__ __forceinline__ void act_apply(float (&v)[N], int32_t act)
 template <int N>
 __device__ __forceinline__ void act_apply_grad(float (&v)[N], float (&d)[N], int32_t act)
 {
+    static_assert(N % 2 == 0, "pairs");
     switch (act) {
         case kActRelu:
 #pragma unroll
@@ -97,35 +138,45 @@ __device__ __forceinline__ void act_apply_grad(float (&v)[N], float (&d)[N], int
         case kActGelu:
             // Phi(x) + x phi(x)
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float e;
-                const float x = v[i], cdf = normal_cdf(x, e);
-                d[i] = fmaf(x * e, 0.3989422804014327f, cdf);
-                v[i] = x * cdf;
+            for (int i = 0; i < N; i += 2) {
+                float q[2], e[2];
+                const float z[2] = {fminf(fabsf(v[i]), 1e4f), fminf(fabsf(v[i + 1]), 1e4f)};
+                normal_tails(v[i], v[i + 1], z[0], z[1], q[0], q[1], e[0], e[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float x = v[i + k];
+                    d[i + k] = fmaf(copysignf(z[k], x) * e[k], 0.3989422804014327f, x < 0.0f ? q[k] : 1.0f - q[k]);
+                    v[i + k] = fmaf(-z[k], q[k], fmaxf(x, 0.0f));
+                }
             }
             break;
         case kActGeluTanh:
-            // p + x p q z'(x), p = sigmoid(z), q = 1 - p, z = C x (1 + A x^2); x^2 is capped where
-            // p q is already 0, so that an overflowing z' cannot make 0 * infinity
+            // p + x p (1 - p) z'(x), p = sigmoid(z), z = C x (1 + A x^2); x^2 is capped where
+            // p (1 - p) is already 0, so that an overflowing z' cannot make 0 * infinity
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float x = v[i];
-                float p, q;
-                sigmoid_both(kGeluC * x * fmaf(kGeluA * x, x, 1.0f), p, q);
-                const float dz = kGeluC * fmaf(3.0f * kGeluA, fminf(x * x, 1e8f), 1.0f);
-                d[i] = fmaf(x * (p * q), dz, p);
-                v[i] = x * p;
+            for (int i = 0; i < N; i += 2) {
+                float p[2], e[2];
+                sigmoids(gelu_tanh_arg(v[i]), gelu_tanh_arg(v[i + 1]), p[0], p[1], e[0], e[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float x = v[i + k];
+                    const float dz = kGeluC * fmaf(3.0f * kGeluA, fminf(x * x, 1e8f), 1.0f);
+                    v[i + k] = x * p[k];
+                    d[i + k] = fmaf(v[i + k] * (p[k] * e[k]), dz, p[k]);
+                }
             }
             break;
         case kActSilu:
-            // p + x p q
+            // p + x p (1 - p)
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float x = v[i];
-                float p, q;
-                sigmoid_both(x, p, q);
-                d[i] = fmaf(x * p, q, p);
-                v[i] = x * p;
+            for (int i = 0; i < N; i += 2) {
+                float p[2], e[2];
+                sigmoids(v[i], v[i + 1], p[0], p[1], e[0], e[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    v[i + k] *= p[k];
+                    d[i + k] = fmaf(v[i + k], p[k] * e[k], p[k]);
+                }
             }
             break;
         default:
@@ -302,37 +353,47 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& ti, 
 
 // ------------------------------------------------------------------ gated product
 
-// One (g, u) pair of h index j of token m, after the reduction; the 16 lanes of a half-warp hold
-// the 16 indices of one block of the same token. `ok`: the token exists. All lanes take part.
+// One value of h (index j of token m), alone or with its half-warp's block.
 template <class Cfg>
-__device__ __forceinline__ void glu_lane(const GemmArgs& a, int m, int j, float g, float u, bool ok)
+__device__ __forceinline__ void glu_put(const GemmArgs& a, int m, int j, float h, bool ok)
 {
-    float v[1] = {g};
+    if constexpr (Cfg::EPI == kEpiGlu) {
+        if (ok) store_out1(a, static_cast<size_t>(m) * a.inter + j, h);
+    } else if constexpr (Cfg::EPI == kEpiGluQuant) {
+        float amax = fabsf(h), rcp;
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const uint32_t sf = block_scale(amax, __ldg(a.gs_h), rcp);
+        const uint32_t code = f32x2_to_e2m1x2(__fmul_rn(h, rcp), 0.0f) & 0xFu;
+        const uint32_t next = __shfl_xor_sync(0xffffffffu, code, 1);
+        if (ok && (j & 1) == 0)
+            a.h_q[static_cast<int64_t>(m) * (a.inter >> 1) + (j >> 1)] = static_cast<uint8_t>(code | (next << 4));
+        if (ok && (j & 15) == 0) *h_sf_at(a, m, j >> 4) = static_cast<uint8_t>(sf);
+    }
+}
+
+// (g, u) pairs of h index j of N tokens m[], after the reduction; the 16 lanes of a half-warp hold
+// the 16 indices of one block of the same token. `ok`: the token exists. All lanes take part.
+template <class Cfg, int N>
+__device__ __forceinline__ void glu_lane(const GemmArgs& a, const int (&m)[N], int j, float (&g)[N], const float (&u)[N],
+                                         const bool (&ok)[N])
+{
     if constexpr (Cfg::EPI == kEpiGluGrad) {
-        float d[1];
-        act_apply_grad(v, d, a.act_fn);
-        if (ok) {
-            const float s = load_side1(a, static_cast<size_t>(m) * a.inter + j);
-            const size_t idx = static_cast<size_t>(m) * a.N + j;
-            store_out1(a, idx, s * u * d[0]);
-            store_out1(a, idx + a.inter, s * v[0]);
+        float d[N], s[N];
+#pragma unroll
+        for (int t = 0; t < N; ++t) s[t] = ok[t] ? load_side1(a, static_cast<size_t>(m[t]) * a.inter + j) : 0.0f;
+        act_apply_grad(g, d, a.act_fn);
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+            if (!ok[t]) continue;
+            const size_t idx = static_cast<size_t>(m[t]) * a.N + j;
+            store_out1(a, idx, s[t] * u[t] * d[t]);
+            store_out1(a, idx + a.inter, s[t] * g[t]);
         }
     } else {
-        act_apply(v, a.act_fn);
-        const float h = v[0] * u;
-        if constexpr (Cfg::EPI == kEpiGlu) {
-            if (ok) store_out1(a, static_cast<size_t>(m) * a.inter + j, h);
-        } else {
-            float amax = fabsf(h), rcp;
+        act_apply(g, a.act_fn);
 #pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const uint32_t sf = block_scale(amax, __ldg(a.gs_h), rcp);
-            const uint32_t code = f32x2_to_e2m1x2(__fmul_rn(h, rcp), 0.0f) & 0xFu;
-            const uint32_t next = __shfl_xor_sync(0xffffffffu, code, 1);
-            if (ok && (j & 1) == 0)
-                a.h_q[static_cast<int64_t>(m) * (a.inter >> 1) + (j >> 1)] = static_cast<uint8_t>(code | (next << 4));
-            if (ok && (j & 15) == 0) *h_sf_at(a, m, j >> 4) = static_cast<uint8_t>(sf);
-        }
+        for (int t = 0; t < N; ++t) glu_put<Cfg>(a, m[t], j, g[t] * u[t], ok[t]);
     }
 }
 
@@ -346,14 +407,20 @@ __device__ __forceinline__ void glu_tok16(const GemmArgs& a, const Tile& ti, int
     const int j0 = (ti.p0 >> 1) + 16 * quad;
     if (j0 >= a.inter) return;                       // warp-uniform
     const bool up = lane >= 16;
+    int m[8];
+    float g[8], u[8];
+    bool ok[8];
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc) {
         const float lo = alpha * __uint_as_float(r[cc]);        // token c + cc
         const float hi = alpha * __uint_as_float(r[cc + 8]);    // token c + 8 + cc
         const float other = __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16);
-        const int m = ti.q0 + c + cc + (up ? 8 : 0);
-        glu_lane<Cfg>(a, m, j0 + (lane & 15), up ? other : lo, up ? hi : other, m < a.M);
+        m[cc] = ti.q0 + c + cc + (up ? 8 : 0);
+        ok[cc] = m[cc] < a.M;
+        g[cc] = up ? other : lo;
+        u[cc] = up ? hi : other;
     }
+    glu_lane<Cfg>(a, m, j0 + (lane & 15), g, u, ok);
 }
 
 // A reduced split-K chunk. Weight-major: item = (32-row group, token, index of the group), so that
@@ -367,16 +434,29 @@ __device__ __forceinline__ void glu_chunk(const GemmArgs& a, const Tile& ti, con
     constexpr int BN = Cfg::BN;
     constexpr int PS = Cfg::PSTRIDE;
     if constexpr (Cfg::SWAP) {
-        for (int item = tid; item < (rows >> 5) * BN * 16; item += 128) {
-            const int i = item & 15, c = (item >> 4) % BN, unit = (item >> 4) / BN;
+        // two tokens per item: c and c + BN / 2
+        for (int item = tid; item < (rows >> 5) * (BN / 2) * 16; item += 128) {
+            const int i = item & 15, c = (item >> 4) % (BN / 2), unit = (item >> 4) / (BN / 2);
             const float* p = src + (32 * unit + i) * PS + c;
-            float g = 0.0f, u = 0.0f;
+            float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
             for (int k = 0; k < nsrc; ++k) {
-                g += p[k * rows * PS];
-                u += p[(k * rows + 16) * PS];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    g[t] += p[k * rows * PS + t * (BN / 2)];
+                    u[t] += p[(k * rows + 16) * PS + t * (BN / 2)];
+                }
             }
-            const int j = ((ti.p0 + r0) >> 1) + 16 * unit + i, m = ti.q0 + c;
-            glu_lane<Cfg>(a, m, j, alpha * g, alpha * u, m < a.M && j < a.inter);
+            const int j = ((ti.p0 + r0) >> 1) + 16 * unit + i;
+            int m[2];
+            bool ok[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                g[t] *= alpha;
+                u[t] *= alpha;
+                m[t] = ti.q0 + c + t * (BN / 2);
+                ok[t] = m[t] < a.M && j < a.inter;
+            }
+            glu_lane<Cfg>(a, m, j, g, u, ok);
         }
     } else {
         constexpr int G = BN / 8;                    // items per row: four indices of h each
