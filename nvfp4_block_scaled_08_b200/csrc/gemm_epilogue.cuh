@@ -538,7 +538,6 @@ struct EpiRows {
     float* const bias_s;         // 64 floats
     uint64_t* const bar;         // side box landed, per buffer
     const int quad, lane, half;
-    const bool f32;
     uint32_t phases = 0;         // bit b: parity of the next wait for buffer b
     uint32_t pending = 0;        // bit b: a side box is on its way into buffer b
     int turn = 0;                // kEpiGlu: the buffer of the next box (a tile can have an odd number)
@@ -549,7 +548,7 @@ struct EpiRows {
                                        uint64_t* bars, const AbortState& abort)
         : a(args), maps(m), ab(abort), buf(smem + (4 * h + q) * Cfg::EPI_WARP),
           bias_s(reinterpret_cast<float*>(smem + kEpilogueWarps * Cfg::EPI_WARP + (4 * h + q) * Cfg::EPI_BIAS)),
-          bar(bars + 2 * (4 * h + q)), quad(q), lane(l), half(h), f32(args.out_dtype == kOutF32)
+          bar(bars + 2 * (4 * h + q)), quad(q), lane(l), half(h)
     {
     }
 
@@ -562,26 +561,27 @@ struct EpiRows {
     }
     __device__ __forceinline__ int chunks(const Tile& ti) const { return (Cfg::NARROW ? ti.q_span : Cfg::BN) / 128; }
 
-    // Boxes of the tile are numbered in the warp's order; `first_col` is the output column (of h
-    // for the gated products) that box u starts at.
-    __device__ __forceinline__ int boxes_per_chunk() const { return LINEAR ? (f32 ? 4 : 2) : (f32 ? 2 : 1); }
-    __device__ __forceinline__ int box_cols() const { return f32 ? 16 : 32; }
+    // Boxes of the tile are numbered in the warp's order, `per_chunk` of them to a chunk; box u
+    // starts at output column first_col (a column of h for the gated products).
+    template <bool F32>
     __device__ __forceinline__ int first_col(const Tile& ti, int u) const
     {
-        const int bpc = boxes_per_chunk(), k = u / bpc;
+        constexpr int per_chunk = (LINEAR ? 2 : 1) * (F32 ? 2 : 1);
+        const int k = u / per_chunk;
         const int c = ti.q0 + chunk_col(ti, k);
-        return (LINEAR ? c : c >> 1) + (u - k * bpc) * box_cols();
+        return (LINEAR ? c : c >> 1) + (u - k * per_chunk) * (F32 ? 16 : 32);
     }
     __device__ __forceinline__ int end_col() const { return LINEAR ? a.N : a.inter; }
 
-    // Lane 0: side box u into buffer b (free). Boxes wholly past the columns are not requested.
+    // Side box u into buffer b (free). Boxes wholly past the columns are not requested.
+    template <bool F32>
     __device__ __forceinline__ void request(const Tile& ti, int u, int b)
     {
-        const int n = first_col(ti, u);
+        const int n = first_col<F32>(ti, u);
         if (n >= end_col()) return;
         if (lane == 0) {
             mbar_arrive_expect_tx(&bar[b], BOX);
-            tma_load_2d(buf + b * BOX, &maps.side, &bar[b], n * (f32 ? 4 : 2), ti.p0 + 32 * quad, l2_policy_evict_first());
+            tma_load_2d(buf + b * BOX, &maps.side, &bar[b], n * (F32 ? 4 : 2), ti.p0 + 32 * quad, l2_policy_evict_first());
         }
         pending |= 1u << b;
     }
@@ -598,14 +598,21 @@ struct EpiRows {
 
     __device__ __forceinline__ bool active(const Tile& ti) const { return ti.p0 + 32 * quad < a.M; }
 
+    template <bool F32>
+    __device__ __forceinline__ void request_first(const Tile& ti)
+    {
+        if (lane == 0) bulk_wait_read<0>();
+        request<F32>(ti, 0, 0);
+        if (LINEAR) request<F32>(ti, 1, 1);          // (GRAD's second buffer takes du)
+    }
+
     __device__ __forceinline__ void begin(const Tile& ti)
     {
         if (!active(ti)) return;
         if constexpr (LINEAR || GRAD) {
             if (a.side != nullptr) {
-                if (lane == 0) bulk_wait_read<0>();
-                request(ti, 0, 0);
-                if (LINEAR) request(ti, 1, 1);       // (GRAD's second buffer takes du)
+                if (a.out_dtype == kOutF32) request_first<true>(ti);
+                else request_first<false>(ti);
             }
         }
         if constexpr (LINEAR) {
@@ -628,12 +635,13 @@ struct EpiRows {
 
     // Buffer b, written by every lane, to output column n. (A box past the columns still makes a
     // bulk group, so that buffers_free<1> means "the other buffer" everywhere.)
+    template <bool F32>
     __device__ __forceinline__ void send(const Tile& ti, int b, int n)
     {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            if (n < end_col()) tma_store_2d(&maps.out, buf + b * BOX, n * (f32 ? 4 : 2), ti.p0 + 32 * quad);
+            if (n < end_col()) tma_store_2d(&maps.out, buf + b * BOX, n * (F32 ? 4 : 2), ti.p0 + 32 * quad);
             bulk_commit();
         }
     }
@@ -646,121 +654,110 @@ struct EpiRows {
         __syncwarp();
     }
 
-    // 16 values as output elements in pieces e0 .. of buffer b (2 pieces of a 16-bit type, 4 of fp32)
-    __device__ __forceinline__ void put16(int b, int e0, const float (&v)[16]) const
+    // NV values as output elements of type DT in pieces e0 .. of buffer b, and back.
+    template <int32_t DT, int NV>
+    __device__ __forceinline__ void put(int b, int e0, const float* v) const
     {
-        if (f32) {
+        constexpr int PER = DT == kOutF32 ? 4 : 8;   // elements per 16-byte piece
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                *slot(b, e) = make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
-                                         __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
-        } else {
-            const int32_t dt = a.out_dtype;
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *slot(b, e0 + e) = make_uint4(pack_out16x2(v[8 * e], v[8 * e + 1], dt), pack_out16x2(v[8 * e + 2], v[8 * e + 3], dt),
-                                              pack_out16x2(v[8 * e + 4], v[8 * e + 5], dt), pack_out16x2(v[8 * e + 6], v[8 * e + 7], dt));
+        for (int e = 0; e < NV / PER; ++e) {
+            const float* x = v + e * PER;
+            if constexpr (DT == kOutF32)
+                *slot(b, e0 + e) = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                              __float_as_uint(x[3]));
+            else
+                *slot(b, e0 + e) = make_uint4(pack_out16x2(x[0], x[1], DT), pack_out16x2(x[2], x[3], DT),
+                                              pack_out16x2(x[4], x[5], DT), pack_out16x2(x[6], x[7], DT));
         }
     }
-    __device__ __forceinline__ void get16(int b, int e0, float (&v)[16]) const
+    template <int32_t DT, int NV>
+    __device__ __forceinline__ void get(int b, int e0, float* v) const
     {
-        if (f32) {
+        constexpr int PER = DT == kOutF32 ? 4 : 8;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint4 x = *slot(b, e);
-                v[4 * e] = __uint_as_float(x.x); v[4 * e + 1] = __uint_as_float(x.y);
-                v[4 * e + 2] = __uint_as_float(x.z); v[4 * e + 3] = __uint_as_float(x.w);
-            }
-        } else {
+        for (int e = 0; e < NV / PER; ++e) {
+            const uint4 q = *slot(b, e0 + e);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint4 x = *slot(b, e0 + e);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack_out16x2(w[i], a.out_dtype);
-                    v[8 * e + 2 * i] = f.x;
-                    v[8 * e + 2 * i + 1] = f.y;
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DT == kOutF32) {
+                    v[e * PER + i] = __uint_as_float(w[i]);
+                } else {
+                    const float2 f = unpack_out16x2(w[i], DT);
+                    v[e * PER + 2 * i] = f.x;
+                    v[e * PER + 2 * i + 1] = f.y;
                 }
             }
         }
     }
 
-    // Piece h (32 columns, r) of chunk k.
+    // Piece h (32 columns, r) of chunk k: one box of a 16-bit type, two of fp32.
+    template <int32_t DT, bool SIDE>
     __device__ __forceinline__ bool linear_piece(const Tile& ti, int k, int h, const uint32_t (&r)[32], float alpha)
     {
-        const int total = chunks(ti) * boxes_per_chunk();
+        constexpr bool F32 = DT == kOutF32;
+        constexpr int BOXES = F32 ? 2 : 1, NV = 32 / BOXES;
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
         linear_act(a.bias != nullptr ? bias_s + 32 * h : nullptr, a.act_fn, alpha, v);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {                // the two halves of the piece: 16 columns each
-            float w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = v[16 * s + i];
-            const int u = f32 ? 4 * k + 2 * h + s : 2 * k + h;
-            const int b = u & 1, e0 = 2 * s;
-            const bool opens = f32 || s == 0, closes = f32 || s == 1;
-            if (opens) {
-                if (a.side != nullptr) {
-                    if (u >= 1 && u + 1 < total) {   // the other buffer is the next box's
-                        buffers_free<0>();
-                        request(ti, u + 1, b ^ 1);
-                    }
-                    if (!landed(b)) return false;
-                } else {
-                    buffers_free<1>();
+        for (int s = 0; s < BOXES; ++s) {
+            const int u = BOXES * (2 * k + h) + s, b = u & 1;
+            if constexpr (SIDE) {
+                if (u >= 1 && u + 1 < 2 * BOXES * chunks(ti)) {   // the other buffer is the next box's
+                    buffers_free<0>();
+                    request<F32>(ti, u + 1, b ^ 1);
                 }
-            }
-            if (a.side != nullptr) {
-                float x[16];
-                get16(b, e0, x);
+                if (!landed(b)) return false;
+                float x[NV];
+                get<DT, NV>(b, 0, x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = fmaf(a.side_scale, x[i], w[i]);
+                for (int i = 0; i < NV; ++i) v[NV * s + i] = fmaf(a.side_scale, x[i], v[NV * s + i]);
+            } else {
+                buffers_free<1>();
             }
-            put16(b, e0, w);
-            if (closes) send(ti, b, first_col(ti, u));
+            put<DT, NV>(b, 0, v + NV * s);
+            send<F32>(ti, b, first_col<F32>(ti, u));
         }
         return true;
     }
 
-    // 16 indices of h from [16 gate, 16 up] columns.
+    // 16 indices of h from [16 gate, 16 up] columns: half a box of a 16-bit type, one of fp32.
+    template <int32_t DT>
     __device__ __forceinline__ bool glu_piece(const Tile& ti, int k, int h, const uint32_t (&r)[32], float alpha,
                                               uint32_t (&q)[4], uint32_t& sf)
     {
-        const int j0 = ((ti.q0 + chunk_col(ti, k)) >> 1) + 16 * h;
+        constexpr bool F32 = DT == kOutF32;
+        const int e0 = F32 ? 0 : 2 * h, u = F32 ? 2 * k + h : k;
         float g[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) g[i] = alpha * __uint_as_float(r[i]);
         if constexpr (GRAD) {
-            const int u = f32 ? 2 * k + h : k, e0 = 2 * h;
-            if ((f32 || h == 0) && u > 0) {
+            if ((F32 || h == 0) && u > 0) {
                 buffers_free<0>();
-                request(ti, u, 0);
+                request<F32>(ti, u, 0);
             }
-            if (!landed(0)) return false;
             float d[16], x[16];
             act_apply_grad(g, d, a.act_fn);
-            get16(0, e0, x);
+            if (!landed(0)) return false;
+            get<DT, 16>(0, e0, x);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 d[i] *= alpha * __uint_as_float(r[16 + i]) * x[i];
                 g[i] *= x[i];
             }
-            put16(0, e0, d);
-            put16(1, e0, g);
-            if (f32 || h == 1) {
-                const int n = first_col(ti, u);
-                if (n < a.inter) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        const int esz = f32 ? 4 : 2;
-                        tma_store_2d(&maps.out, buf, n * esz, ti.p0 + 32 * quad);
-                        tma_store_2d(&maps.out, buf + BOX, (a.inter + n) * esz, ti.p0 + 32 * quad);
-                        bulk_commit();
-                    }
+            put<DT, 16>(0, e0, d);
+            put<DT, 16>(1, e0, g);
+            if (F32 || h == 1) {
+                const int n = first_col<F32>(ti, u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && n < a.inter) {
+                    constexpr int esz = F32 ? 4 : 2;
+                    tma_store_2d(&maps.out, buf, n * esz, ti.p0 + 32 * quad);
+                    tma_store_2d(&maps.out, buf + BOX, (a.inter + n) * esz, ti.p0 + 32 * quad);
+                    bulk_commit();
                 }
             }
             return true;
@@ -770,6 +767,7 @@ struct EpiRows {
         for (int i = 0; i < 16; ++i) g[i] *= alpha * __uint_as_float(r[16 + i]);
         if constexpr (QUANT) {
             // one NVFP4 block per piece; a row's two blocks of a chunk leave together
+            const int j0 = ((ti.q0 + chunk_col(ti, k)) >> 1) + 16 * h;
             float amax = 0.0f, rcp, lo[8], hi[8];
 #pragma unroll
             for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(g[i]));
@@ -791,10 +789,10 @@ struct EpiRows {
                 }
             }
         } else {
-            if (f32 || h == 0) buffers_free<1>();
-            put16(turn, 2 * h, g);
-            if (f32 || h == 1) {
-                send(ti, turn, first_col(ti, f32 ? 2 * k + h : k));
+            if (F32 || h == 0) buffers_free<1>();
+            put<DT, 16>(turn, e0, g);
+            if (F32 || h == 1) {
+                send<F32>(ti, turn, first_col<F32>(ti, u));
                 turn ^= 1;
             }
         }
@@ -802,14 +800,12 @@ struct EpiRows {
     }
 
     // Drains the tile from TMEM (tacc: this warp's lanes and the accumulator's first column);
-    // `drained` is called once the first chunk is in registers.
-    template <class F>
-    __device__ __forceinline__ bool finish(const Tile& ti, uint32_t tacc, float alpha, F drained)
+    // `drained` is called once the first chunk is in registers. The output type and the side
+    // input are decided once per tile: branches inside would cut the code into blocks too short
+    // to hide its latencies with two warps to a scheduler.
+    template <int32_t DT, bool SIDE, class F>
+    __device__ __forceinline__ bool finish_as(const Tile& ti, uint32_t tacc, float alpha, F drained)
     {
-        if (!active(ti)) {
-            drained();
-            return true;
-        }
         uint32_t q[4], sf = 0;
         bool ok = true;
         const int nk = chunks(ti);
@@ -832,13 +828,36 @@ struct EpiRows {
             for (int i = 0; i < 32; ++i) cur[i] = r[i >> 4][i & 15];
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                if constexpr (LINEAR) ok = ok && linear_piece(ti, k, h, cur, alpha);
-                else ok = ok && glu_piece(ti, k, h, cur, alpha, q, sf);
+                if constexpr (LINEAR) ok = ok && linear_piece<DT, SIDE>(ti, k, h, cur, alpha);
+                else ok = ok && glu_piece<DT>(ti, k, h, cur, alpha, q, sf);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) cur[i] = r[2 + (i >> 4)][i & 15];
             }
         }
         return __all_sync(0xffffffffu, ok);
+    }
+
+    template <int32_t DT, class F>
+    __device__ __forceinline__ bool finish_type(const Tile& ti, uint32_t tacc, float alpha, F drained)
+    {
+        if constexpr (LINEAR) {
+            if (a.side == nullptr) return finish_as<DT, false>(ti, tacc, alpha, drained);
+        }
+        return finish_as<DT, true>(ti, tacc, alpha, drained);
+    }
+
+    template <class F>
+    __device__ __forceinline__ bool finish(const Tile& ti, uint32_t tacc, float alpha, F drained)
+    {
+        if (!active(ti)) {
+            drained();
+            return true;
+        }
+        if constexpr (!QUANT) {
+            if (a.out_dtype == kOutF32) return finish_type<kOutF32>(ti, tacc, alpha, drained);
+            if (a.out_dtype == kOutF16) return finish_type<kOutF16>(ti, tacc, alpha, drained);
+        }
+        return finish_type<kOutBF16>(ti, tacc, alpha, drained);
     }
 
     // Before the CTA's shared memory is released: every box has landed and every store has read.
