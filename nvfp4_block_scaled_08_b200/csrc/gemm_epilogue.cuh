@@ -28,50 +28,59 @@ __device__ __forceinline__ float exp2_approx(float x)          // 2^-22 relative
     return y;
 }
 
-// t = 1 / d of two values of 1 .. 2^61
-__device__ __forceinline__ void reciprocals(float d0, float d1, float& t0, float& t1)
+// 1 / d of two values of 1 .. 2^61
+__device__ __forceinline__ f32x2 reciprocals(f32x2 d)
 {
-    float r;
+    float d0, d1, r;
+    unpack2(d, d0, d1);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d0 * d1));
-    t0 = r * d1;
-    t1 = r * d0;
+    return mul2(pack2(r, r), pack2(d1, d0));
 }
 
-// p = sigmoid(x) = 1 / (1 + e) of two values, with e = exp(-x). e is capped at 2^60, where p is
-// negligible; 1 - p is p e (1 - p itself would lose it where p is near 1).
-__device__ __forceinline__ void sigmoids(float x0, float x1, float& p0, float& p1, float& e0, float& e1)
+// sigmoid(x) = 1 / (1 + e) of two values, and e = exp(-x), capped at 2^60, where the sigmoid is
+// negligible; 1 - sigmoid is their product (the difference would lose it where it is near 0).
+__device__ __forceinline__ f32x2 sigmoids(f32x2 x, f32x2& e)
 {
     constexpr float kLog2e = 1.4426950408889634f;
-    e0 = exp2_approx(fminf(-kLog2e * x0, 60.0f));
-    e1 = exp2_approx(fminf(-kLog2e * x1, 60.0f));
-    reciprocals(1.0f + e0, 1.0f + e1, p0, p1);
+    float y0, y1;
+    unpack2(mul2(x, pack2(-kLog2e, -kLog2e)), y0, y1);
+    e = pack2(exp2_approx(fminf(y0, 60.0f)), exp2_approx(fminf(y1, 60.0f)));
+    return reciprocals(add2(e, pack2(1.0f, 1.0f)));
 }
 
 // gelu_tanh(x) = x sigmoid(C x (1 + A x^2)), since (1 + tanh z) / 2 = sigmoid(2 z)
 constexpr float kGeluC = 1.5957691216057308f, kGeluA = 0.044715f;   // C = 2 sqrt(2 / pi)
-__device__ __forceinline__ float gelu_tanh_arg(float x) { return kGeluC * x * fmaf(kGeluA * x, x, 1.0f); }
+__device__ __forceinline__ f32x2 gelu_tanh_arg(f32x2 x)
+{
+    return mul2(mul2(x, pack2(kGeluC, kGeluC)), fma2(mul2(x, pack2(kGeluA, kGeluA)), x, pack2(1.0f, 1.0f)));
+}
 
 // Q(z) = 1 - Phi(z), Phi the normal distribution function, of z = min(|x|, 10^4), and e =
 // exp(-x^2 / 2), for two values. With t = 1 / (1 + p w), w = z / sqrt 2: erfc(w) = (a1 t + ... +
 // a5 t^5) exp(-w^2) + d, |d| <= 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical
 // Functions, 7.1.26): Q is within 2^-23, with no 1 - erf to cancel.
-__device__ __forceinline__ void normal_tails(float x0, float x1, float z0, float z1, float& q0, float& q1, float& e0,
-                                             float& e1)
+__device__ __forceinline__ f32x2 normal_tails(f32x2 x, f32x2& z, f32x2& e)
 {
     constexpr float kHalfLog2e = 0.72134752044448170f, kP = 0.3275911f * 0.70710678118654752f;
-    e0 = exp2_approx(-kHalfLog2e * x0 * x0);
-    e1 = exp2_approx(-kHalfLog2e * x1 * x1);
-    float t[2], q[2];
-    reciprocals(fmaf(kP, z0, 1.0f), fmaf(kP, z1, 1.0f), t[0], t[1]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {       // (the coefficients halved)
-        q[i] = fmaf(t[i], 0.5307027145f, -0.7265760135f);
-        q[i] = fmaf(t[i], q[i], 0.7107068705f);
-        q[i] = fmaf(t[i], q[i], -0.142248368f);
-        q[i] = fmaf(t[i], q[i], 0.127414796f) * t[i];
-    }
-    q0 = q[0] * e0;
-    q1 = q[1] * e1;
+    float x0, x1, y0, y1;
+    unpack2(x, x0, x1);
+    z = pack2(fminf(fabsf(x0), 1e4f), fminf(fabsf(x1), 1e4f));
+    unpack2(mul2(mul2(x, x), pack2(-kHalfLog2e, -kHalfLog2e)), y0, y1);
+    e = pack2(exp2_approx(y0), exp2_approx(y1));
+    const f32x2 t = reciprocals(fma2(z, pack2(kP, kP), pack2(1.0f, 1.0f)));
+    f32x2 q = fma2(t, pack2(0.5307027145f, 0.5307027145f), pack2(-0.7265760135f, -0.7265760135f));   // (a5 .. a1 halved)
+    q = fma2(t, q, pack2(0.7107068705f, 0.7107068705f));
+    q = fma2(t, q, pack2(-0.142248368f, -0.142248368f));
+    q = fma2(t, q, pack2(0.127414796f, 0.127414796f));
+    return mul2(mul2(q, t), e);
+}
+
+// x Phi(x) = max(x, 0) - |x| Q(|x|)
+__device__ __forceinline__ f32x2 gelu_of(f32x2 x, f32x2 z, f32x2 q)
+{
+    float x0, x1;
+    unpack2(x, x0, x1);
+    return fma2(mul2(z, pack2(-1.0f, -1.0f)), q, pack2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
 }
 
 // v = act(v) for all elements (the switch is uniform, one branch per array).
@@ -89,32 +98,27 @@ __device__ __forceinline__ void act_apply(float (&v)[N], int32_t act)
             for (int i = 0; i < N; ++i) { const float p = v[i] < 0.0f ? 0.0f : v[i]; v[i] = p * p; }
             break;
         case kActGelu:
-            // x Phi(x) = max(x, 0) - |x| Q(|x|)
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                float q[2], e[2];
-                const float z[2] = {fminf(fabsf(v[i]), 1e4f), fminf(fabsf(v[i + 1]), 1e4f)};
-                normal_tails(v[i], v[i + 1], z[0], z[1], q[0], q[1], e[0], e[1]);
-                v[i] = fmaf(-z[0], q[0], fmaxf(v[i], 0.0f));
-                v[i + 1] = fmaf(-z[1], q[1], fmaxf(v[i + 1], 0.0f));
+                f32x2 z, e;
+                const f32x2 x = pack2(v[i], v[i + 1]), q = normal_tails(x, z, e);
+                unpack2(gelu_of(x, z, q), v[i], v[i + 1]);
             }
             break;
         case kActGeluTanh:
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                float p[2], e[2];
-                sigmoids(gelu_tanh_arg(v[i]), gelu_tanh_arg(v[i + 1]), p[0], p[1], e[0], e[1]);
-                v[i] *= p[0];
-                v[i + 1] *= p[1];
+                f32x2 e;
+                const f32x2 x = pack2(v[i], v[i + 1]);
+                unpack2(mul2(x, sigmoids(gelu_tanh_arg(x), e)), v[i], v[i + 1]);
             }
             break;
         case kActSilu:
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                float p[2], e[2];
-                sigmoids(v[i], v[i + 1], p[0], p[1], e[0], e[1]);
-                v[i] *= p[0];
-                v[i + 1] *= p[1];
+                f32x2 e;
+                const f32x2 x = pack2(v[i], v[i + 1]);
+                unpack2(mul2(x, sigmoids(x, e)), v[i], v[i + 1]);
             }
             break;
         default: break;
@@ -139,15 +143,15 @@ __device__ __forceinline__ void act_apply_grad(float (&v)[N], float (&d)[N], int
             // Phi(x) + x phi(x)
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                float q[2], e[2];
-                const float z[2] = {fminf(fabsf(v[i]), 1e4f), fminf(fabsf(v[i + 1]), 1e4f)};
-                normal_tails(v[i], v[i + 1], z[0], z[1], q[0], q[1], e[0], e[1]);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float x = v[i + k];
-                    d[i + k] = fmaf(copysignf(z[k], x) * e[k], 0.3989422804014327f, x < 0.0f ? q[k] : 1.0f - q[k]);
-                    v[i + k] = fmaf(-z[k], q[k], fmaxf(x, 0.0f));
-                }
+                f32x2 z, e;
+                const f32x2 x = pack2(v[i], v[i + 1]), q = normal_tails(x, z, e);
+                float q0, q1, z0, z1;
+                unpack2(q, q0, q1);
+                unpack2(z, z0, z1);
+                const f32x2 cdf = pack2(v[i] < 0.0f ? q0 : 1.0f - q0, v[i + 1] < 0.0f ? q1 : 1.0f - q1);
+                const f32x2 xe = mul2(pack2(copysignf(z0, v[i]), copysignf(z1, v[i + 1])), e);
+                unpack2(fma2(xe, pack2(0.3989422804014327f, 0.3989422804014327f), cdf), d[i], d[i + 1]);
+                unpack2(gelu_of(x, z, q), v[i], v[i + 1]);
             }
             break;
         case kActGeluTanh:
@@ -155,28 +159,23 @@ __device__ __forceinline__ void act_apply_grad(float (&v)[N], float (&d)[N], int
             // p (1 - p) is already 0, so that an overflowing z' cannot make 0 * infinity
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                float p[2], e[2];
-                sigmoids(gelu_tanh_arg(v[i]), gelu_tanh_arg(v[i + 1]), p[0], p[1], e[0], e[1]);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float x = v[i + k];
-                    const float dz = kGeluC * fmaf(3.0f * kGeluA, fminf(x * x, 1e8f), 1.0f);
-                    v[i + k] = x * p[k];
-                    d[i + k] = fmaf(v[i + k] * (p[k] * e[k]), dz, p[k]);
-                }
+                f32x2 e;
+                const f32x2 x = pack2(v[i], v[i + 1]), p = sigmoids(gelu_tanh_arg(x), e);
+                const f32x2 xx = pack2(fminf(v[i] * v[i], 1e8f), fminf(v[i + 1] * v[i + 1], 1e8f));
+                const f32x2 dz = fma2(xx, pack2(3.0f * kGeluA * kGeluC, 3.0f * kGeluA * kGeluC), pack2(kGeluC, kGeluC));
+                const f32x2 xp = mul2(x, p);
+                unpack2(fma2(mul2(xp, mul2(p, e)), dz, p), d[i], d[i + 1]);
+                unpack2(xp, v[i], v[i + 1]);
             }
             break;
         case kActSilu:
             // p + x p (1 - p)
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                float p[2], e[2];
-                sigmoids(v[i], v[i + 1], p[0], p[1], e[0], e[1]);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    v[i + k] *= p[k];
-                    d[i + k] = fmaf(v[i + k], p[k] * e[k], p[k]);
-                }
+                f32x2 e;
+                const f32x2 x = pack2(v[i], v[i + 1]), p = sigmoids(x, e), xp = mul2(x, p);
+                unpack2(fma2(xp, mul2(p, e), p), d[i], d[i + 1]);
+                unpack2(xp, v[i], v[i + 1]);
             }
             break;
         default:
@@ -260,18 +259,17 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float gs, float& r)
 template <int N>
 __device__ __forceinline__ void linear_act(const float* bias, int32_t act, float alpha, float (&v)[N])
 {
+    const f32x2 al = pack2(alpha, alpha);
     if (bias != nullptr) {
 #pragma unroll
         for (int k = 0; k < N; k += 4) {
             const float4 b = *reinterpret_cast<const float4*>(bias + k);
-            v[k] = fmaf(alpha, v[k], b.x);
-            v[k + 1] = fmaf(alpha, v[k + 1], b.y);
-            v[k + 2] = fmaf(alpha, v[k + 2], b.z);
-            v[k + 3] = fmaf(alpha, v[k + 3], b.w);
+            unpack2(fma2(al, pack2(v[k], v[k + 1]), pack2(b.x, b.y)), v[k], v[k + 1]);
+            unpack2(fma2(al, pack2(v[k + 2], v[k + 3]), pack2(b.z, b.w)), v[k + 2], v[k + 3]);
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] *= alpha;
+        for (int k = 0; k < N; k += 2) unpack2(mul2(al, pack2(v[k], v[k + 1])), v[k], v[k + 1]);
     }
     act_apply(v, act);
 }
@@ -542,6 +540,11 @@ struct EpiRows {
     uint32_t pending = 0;        // bit b: a side box is on its way into buffer b
     int turn = 0;                // kEpiGlu: the buffer of the next box (a tile can have an odd number)
     float2 bias[2];              // of chunk 0 and 1, two columns per lane
+    // kEpiGluGrad: a second chunk's 16-bit dh box waits in registers until its buffer is free, four
+    // 16-byte pieces per lane as they come from memory (piece lane % 4 of rows lane / 4 + 8 t).
+    // (8192 x 2048 x 6144: 87 against 89 us with a load once the buffer is free. For kEpiLinear,
+    // whose two late boxes take twice the registers, the load is faster: 69 against 72 us.)
+    uint4 late[GRAD ? 4 : 1];
 
     // smem: the boxes of all epilogue warps (512-byte aligned, as their swizzle is), then their biases
     __device__ __forceinline__ EpiRows(const GemmArgs& args, const EpiMaps<true>& m, int q, int l, int h, uint8_t* smem,
@@ -598,12 +601,34 @@ struct EpiRows {
 
     __device__ __forceinline__ bool active(const Tile& ti) const { return ti.p0 + 32 * quad < a.M; }
 
+    // What the tile reads first: the boxes that fit the buffers, and the late ones.
     template <bool F32>
     __device__ __forceinline__ void request_first(const Tile& ti)
     {
         if (lane == 0) bulk_wait_read<0>();
         request<F32>(ti, 0, 0);
         if (LINEAR) request<F32>(ti, 1, 1);          // (GRAD's second buffer takes du)
+        if (GRAD && !F32 && chunks(ti) == 2) {
+            const int n = first_col<false>(ti, 1) + 8 * (lane & 3);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int64_t m = ti.p0 + 32 * quad + (lane >> 2) + 8 * t;
+                late[t] = make_uint4(0u, 0u, 0u, 0u);
+                if (m < a.M && n < a.inter)
+                    late[t] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.side) + m * a.inter + n);
+            }
+        }
+    }
+
+    // The late box into buffer 0 (free).
+    __device__ __forceinline__ void late_box()
+    {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int r = (lane >> 2) + 8 * t;
+            *reinterpret_cast<uint4*>(buf + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)) = late[t];
+        }
+        __syncwarp();
     }
 
     __device__ __forceinline__ void begin(const Tile& ti)
@@ -712,8 +737,12 @@ struct EpiRows {
                 if (!landed(b)) return false;
                 float x[NV];
                 get<DT, NV>(b, 0, x);
+                const f32x2 sc = pack2(a.side_scale, a.side_scale);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) v[NV * s + i] = fmaf(a.side_scale, x[i], v[NV * s + i]);
+                for (int i = 0; i < NV; i += 2) {
+                    float* w = v + NV * s + i;
+                    unpack2(fma2(sc, pack2(x[i], x[i + 1]), pack2(w[0], w[1])), w[0], w[1]);
+                }
             } else {
                 buffers_free<1>();
             }
@@ -730,22 +759,28 @@ struct EpiRows {
     {
         constexpr bool F32 = DT == kOutF32;
         const int e0 = F32 ? 0 : 2 * h, u = F32 ? 2 * k + h : k;
-        float g[16];
+        const f32x2 al = pack2(alpha, alpha);
+        float g[16], w[16];                          // g and u
 #pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = alpha * __uint_as_float(r[i]);
+        for (int i = 0; i < 16; i += 2) {
+            unpack2(mul2(al, pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]))), g[i], g[i + 1]);
+            unpack2(mul2(al, pack2(__uint_as_float(r[16 + i]), __uint_as_float(r[17 + i]))), w[i], w[i + 1]);
+        }
         if constexpr (GRAD) {
             if ((F32 || h == 0) && u > 0) {
                 buffers_free<0>();
-                request<F32>(ti, u, 0);
+                if constexpr (F32) request<F32>(ti, u, 0);
+                else late_box();
             }
             float d[16], x[16];
             act_apply_grad(g, d, a.act_fn);
             if (!landed(0)) return false;
             get<DT, 16>(0, e0, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                d[i] *= alpha * __uint_as_float(r[16 + i]) * x[i];
-                g[i] *= x[i];
+            for (int i = 0; i < 16; i += 2) {
+                const f32x2 s = pack2(x[i], x[i + 1]);
+                unpack2(mul2(mul2(pack2(d[i], d[i + 1]), pack2(w[i], w[i + 1])), s), d[i], d[i + 1]);
+                unpack2(mul2(pack2(g[i], g[i + 1]), s), g[i], g[i + 1]);
             }
             put<DT, 16>(0, e0, d);
             put<DT, 16>(1, e0, g);
@@ -764,7 +799,7 @@ struct EpiRows {
         }
         act_apply(g, a.act_fn);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] *= alpha * __uint_as_float(r[16 + i]);
+        for (int i = 0; i < 16; i += 2) unpack2(mul2(pack2(g[i], g[i + 1]), pack2(w[i], w[i + 1])), g[i], g[i + 1]);
         if constexpr (QUANT) {
             // one NVFP4 block per piece; a row's two blocks of a chunk leave together
             const int j0 = ((ti.q0 + chunk_col(ti, k)) >> 1) + 16 * h;
