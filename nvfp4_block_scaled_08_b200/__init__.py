@@ -139,7 +139,7 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
 
 
 def _check(fn: str, status: int):
-    if status != 0:
+    if status:
         msg = load().nvfp4_status_string(status).decode()
         raise Nvfp4Error(fn, status, msg)
 
@@ -447,13 +447,20 @@ def _tiled_bytes(rows: int, K: int) -> int:
 def _operands(Aq, sfA, Bq, sfB, alpha_t):
     """Checked addresses of A and B with tiled scales and alpha, and (M, N, K, device index)."""
     dev = _current_device(Aq, "Aq")
-    (M, k2), (N, kb2), u8 = Aq.shape, Bq.shape, torch.uint8
+    (M, k2), (N, kb2) = Aq.shape, Bq.shape
     if k2 != kb2:
         raise ValueError("Aq and Bq must be [rows, K/2] with the same K")
-    K = 2 * k2
-    return (_arg(Aq, "Aq", u8, dev), _arg(sfA, "sfA", u8, dev, None, _tiled_bytes(M, K)),
-            _arg(Bq, "Bq", u8, dev), _arg(sfB, "sfB", u8, dev, None, _tiled_bytes(N, K)),
-            _arg(alpha_t, "alpha", torch.float32, dev, None, 1)), M, N, K, dev
+    u8, f32, K = torch.uint8, torch.float32, 2 * k2
+    nA, nB = (M + 127) // 128 * 128 * (K // 16), (N + 127) // 128 * 128 * (K // 16)
+    # one test of everything (a call each for the five costs a microsecond); what failed is said below
+    if not (Aq.dtype is u8 and Bq.dtype is u8 and sfA.dtype is u8 and sfB.dtype is u8 and alpha_t.dtype is f32
+            and dev == Bq.get_device() == sfA.get_device() == sfB.get_device() == alpha_t.get_device()
+            and Aq.is_contiguous() and Bq.is_contiguous() and sfA.is_contiguous() and sfB.is_contiguous()
+            and sfA.numel() >= nA and sfB.numel() >= nB and alpha_t.numel() >= 1 and alpha_t.is_contiguous()):
+        for t, name, dtype, n in ((Aq, "Aq", u8, 0), (sfA, "sfA", u8, nA), (Bq, "Bq", u8, 0), (sfB, "sfB", u8, nB),
+                                  (alpha_t, "alpha", f32, 1)):
+            _arg(t, name, dtype, dev, None, n)
+    return (Aq.data_ptr(), sfA.data_ptr(), Bq.data_ptr(), sfB.data_ptr(), alpha_t.data_ptr()), M, N, K, dev
 
 
 def gemm_epilogue(Aq, sfA, Bq, sfB, alpha_t, out=None, *, bias=None, act: str = "none", residual=None,

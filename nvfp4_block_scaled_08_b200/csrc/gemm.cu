@@ -146,14 +146,19 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool allow_workspace, int nu
     return p;
 }
 
-// The fused products run few-token tiles as the plain product does, and otherwise 128-wide tiles
-// (with or without a split-K cluster) or 256-wide CTA pairs, whichever a model of its measured
-// times puts first. With nk K stages, in us on B200, beside about 3 us per launch:
-//   a round of 256 x 256 pair tiles  0.388 nk + 2.1   (8192 x 4096 x 6144: 7 rounds, 80 measured)
-//   a wave of 128 x 128 tiles        0.30 nk + 1.1    (same: 14 waves, 116; 500 x 2048 x 6144: 11.3)
-//   the same split over cs CTAs      0.30 nk / cs + 4.9  (500 x 2048 x 6144, cs = 2: 11.5)
-// Where they cross: 700 x 4096 x 6144 one round of pairs 14.5, two waves 19.6; 1024 x 6144 x 2048
-// two rounds 11.5, three waves 13.1; 500 x 2048 x 6144 one round 13.2, one wave 11.3.
+// The fused products run few-token tiles as the plain product does, and otherwise 128 x 128 tiles
+// (with or without a split-K cluster) or CTA pairs on 256 x 128 or 256 x 256 tiles, whichever a
+// model of the measured times puts first. With nk K stages, in us on B200, beside about 3 us per
+// launch (M x N x K; measured times in brackets):
+//   a wave of 128 x 128 tiles           0.30 nk + 1.1      (500 x 2048 x 6144, one: 11.2)
+//   the same split over cs CTAs         0.30 nk / cs + 4.9 (the same, cs = 2: 11.6; 100 x 768 x 6144, cs = 8: 8.7)
+//   a round of 256 x 128 pair tiles     0.235 nk + 1.9     (500 x 2048 x 6144, one: 10.2; 1024 x 4096 x 6144, two: 17.5)
+//   a round of 256 x 256 pair tiles     0.388 nk + 2.1     (1024 x 4096 x 6144, one: 14.5; 500 x 2048 x 6144, one: 12.5;
+//                                       0.6 of it for a last one run as halves: 1500 x 4096 x 6144: 20.9;
+//                                       0.85 where the halves are all there is)
+// Where they cross: 200 x 6144 x 2048 one wave 6.6, one round of 256 x 128 6.9, of 256 x 256 8.0;
+// 700 x 4096 x 6144 two waves 19.1, two rounds 16.5, one round 14.0; 100 x 768 x 6144 one wave
+// 10.3, split 8.7.
 GemmPlan plan_fused(int64_t M, int64_t N, int64_t K, int num_sms)
 {
     GemmPlan p = plan_gemm(M, N, K, false, num_sms);
@@ -163,8 +168,8 @@ GemmPlan plan_fused(int64_t M, int64_t N, int64_t K, int num_sms)
     const int fc = g_force_cluster.load(std::memory_order_relaxed);
     const int fp = g_force_pair.load(std::memory_order_relaxed);
     if (force == 192 || force == 224) return p;          // refused by the caller: linear scales only
-    const int pairs = (p.p_tiles + 1) / 2 * ceil_div(N, 256), clusters = std::max(1, max_active_clusters(2));
-    const int tiles = p.p_tiles * ceil_div(N, 128);
+    const int clusters = std::max(1, max_active_clusters(2));
+    const int tiles = p.p_tiles * ceil_div(N, 128), rows2 = (p.p_tiles + 1) / 2;
     int cs = 1;
     if (fc > 0) {
         cs = std::min({fc, 8, nk});
@@ -173,23 +178,35 @@ GemmPlan plan_fused(int64_t M, int64_t N, int64_t K, int num_sms)
             if (tiles <= max_active_clusters(c)) { cs = c; break; }
         }
     }
-    const double wave = 0.30 * nk + 1.1, split = 0.30 * nk / cs + 4.9;
-    const double t128 = ceil_div(tiles, num_sms) * wave;
-    if (fc <= 0 && split >= t128) cs = 1;
-    const double t256 = ceil_div(pairs, clusters) * (0.388 * nk + 2.1);
-    // an override of the width, the cluster or the pairs decides what it names
-    bool pair = t256 < (cs > 1 ? split : t128);
-    if (force == 128 || (force == 0 && fc > 1)) pair = false;
-    if (force == 256 || (force == 0 && fp == 2)) pair = true;
-    if (fp == 1 || (fc > 1 && force == 256) || p.p_tiles < 2) pair = false;
-    p.bn = pair ? 256 : 128;
-    p.pair = pair;
+    const int pairs256 = rows2 * ceil_div(N, 256), tail = pairs256 % clusters;
+    const double rounds256 = pairs256 / clusters + (tail == 0 ? 0.0 : 2 * tail > clusters ? 1.0 : pairs256 > tail ? 0.6 : 0.85);
+    // candidates: {tile width, pairs, split-K CTAs, time}; an override rules out what it excludes
+    struct Choice { int bn; bool pair; int cs; double us; };
+    const Choice choices[] = {
+        {128, false, 1, ceil_div(tiles, num_sms) * (0.30 * nk + 1.1)},
+        {128, false, cs, 0.30 * nk / cs + 4.9},
+        {128, true, 1, ceil_div(rows2 * ceil_div(N, 128), clusters) * (0.235 * nk + 1.9)},
+        {256, true, 1, rounds256 * (0.388 * nk + 2.1)},
+    };
+    const Choice* best = nullptr;
+    for (const Choice& c : choices) {
+        if (c.pair && (fp == 1 || p.p_tiles < 2 || fc > 1)) continue;
+        if (!c.pair && fp == 2 && p.p_tiles >= 2 && fc <= 1) continue;
+        if (c.pair && force != 0 && c.bn != force) continue;
+        if (!c.pair && force == 256 && fp != 1 && p.p_tiles >= 2 && fc <= 1) continue;
+        if (!c.pair && fc > 0 && c.cs != cs) continue;
+        if (&c == &choices[1] && cs == 1) continue;      // no cluster to split over: the first choice
+        if (!best || c.us < best->us) best = &c;
+    }
+    if (!best) best = &choices[0];
+    p.bn = best->bn;
+    p.pair = best->pair;
     p.q_tiles = ceil_div(N, p.bn);
-    p.cluster = pair ? 1 : cs;
+    p.cluster = best->cs;
     p.splits = p.cluster;
     p.num_tiles = p.p_tiles * p.q_tiles * p.splits;
     p.grid = p.splits > 1 ? p.num_tiles : std::min(p.num_tiles, num_sms);
-    if (pair) plan_pairs(p, fp != 3);
+    if (p.pair) plan_pairs(p, fp != 3);
     return p;
 }
 

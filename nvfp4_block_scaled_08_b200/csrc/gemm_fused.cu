@@ -19,6 +19,8 @@ static cudaError_t launch_epi(const GemmPlan& plan, const GemmLaunch& L, cudaStr
     }
     if (plan.pair && plan.bn == 256)
         return run<256, false, false, true, false, false, true, false, EPI>(plan, L, stream, encode_failed);
+    if (plan.pair && plan.bn == 128)
+        return run<128, false, false, true, false, false, true, false, EPI>(plan, L, stream, encode_failed);
     if (plan.bn == 128) return run<128, false, false, true, false, false, false, false, EPI>(plan, L, stream, encode_failed);
     return cudaErrorInvalidValue;
 }

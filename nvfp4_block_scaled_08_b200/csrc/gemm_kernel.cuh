@@ -178,9 +178,9 @@ struct GemmCfg {
     // the (g, u) pairs of one 16-element block of h; its tiled scales are stored in that order.
     static constexpr int EPI = EPI_;
     static constexpr bool GLU = EPI >= kEpiGlu;
-    static_assert(EPI == kEpiPlain || (SFT && !GROUPED && !MX && !ACTQ && (SWAP || BN == (PAIR ? 256 : 128))),
+    static_assert(EPI == kEpiPlain || (SFT && !GROUPED && !MX && !ACTQ && (SWAP || PAIR || BN == 128)),
                   "fused epilogues serve the dense NVFP4 product with tiled scales: few-token tiles, "
-                  "128-wide tiles and 256-wide CTA pairs");
+                  "128-wide tiles and CTA pairs");
     static constexpr bool EPI_ROWS = EPI != kEpiPlain && !SWAP;   // token-major fused tiles
     static constexpr int ACTQ_BYTES = ACTQ ? 1024 + 64 + 64 : 0;   // gs / e4m3 table, maxima slots, reduction
     static_assert(!SFT || BN % 128 == 0 || (SWAP && BN <= 64), "Q tiles on 128-row tile boundaries");
@@ -1127,6 +1127,10 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             prefetch_tensormap(&tm_sfq);
         }
         if constexpr (Cfg::NARROW) prefetch_tensormap(&tm_q_half);
+        if constexpr (Cfg::EPI_ROWS && Cfg::EPI != kEpiGluQuant) {
+            prefetch_tensormap(&tm_epi.out);
+            if (args.side != nullptr) prefetch_tensormap(&tm_epi.side);
+        }
     }
     if (warp == 1) {
         if constexpr (Cfg::PAIR) {
