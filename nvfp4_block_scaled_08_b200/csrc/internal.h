@@ -67,6 +67,7 @@ struct NormLaunch {
     void* out; int32_t out_dt;                  // [rows][H], or
     uint8_t* q; uint8_t* sf; const float* gs;   // NVFP4 codes and scales (q not null)
     int32_t sf_tiled;
+    int32_t wide;                               // set by the launch: 32-byte accesses
 };
 cudaError_t launch_residual_norm(const NormLaunch& a, cudaStream_t stream, int num_sms);
 

@@ -38,15 +38,37 @@ __device__ __forceinline__ uint4 load16(const void* p)
     return v;
 }
 
+// Eight fp32 values (a lane's 32 bytes beside the next lane's) as one access where the address
+// allows (`wide`: 32-byte aligned), else as two: two 16-byte accesses 32 bytes apart use half of
+// each 128-byte line that they pass L1 with.
+__device__ __forceinline__ void load32(const float* p, bool wide, uint4& lo, uint4& hi)
+{
+    if (wide) {
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
+                     : "l"(p)
+                     : "memory");
+    } else {
+        lo = load16(p);
+        hi = load16(p + 4);
+    }
+}
+
 // Eight consecutive elements as they sit in memory, and their values.
 template <typename T> struct Vec8;
 template <> struct Vec8<float> {
     uint4 lo, hi;
-    __device__ void load(const float* p) { lo = load16(p); hi = load16(p + 4); }
-    __device__ void store(float* p) const
+    __device__ void load(const float* p, bool wide) { load32(p, wide, lo, hi); }
+    __device__ void store(float* p, bool wide) const
     {
-        reinterpret_cast<uint4*>(p)[0] = lo;
-        reinterpret_cast<uint4*>(p)[1] = hi;
+        if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                         ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                         : "memory");
+        } else {
+            reinterpret_cast<uint4*>(p)[0] = lo;
+            reinterpret_cast<uint4*>(p)[1] = hi;
+        }
     }
     __device__ void decode(float (&v)[8]) const { InTraits<float>::decode(Raw32{lo, hi}, v); }
     __device__ void encode(const float (&v)[8])
@@ -57,8 +79,8 @@ template <> struct Vec8<float> {
 };
 template <> struct Vec8<__nv_bfloat16> {
     uint4 u;
-    __device__ void load(const __nv_bfloat16* p) { u = load16(p); }
-    __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+    __device__ void load(const __nv_bfloat16* p, bool) { u = load16(p); }
+    __device__ void store(__nv_bfloat16* p, bool) const { *reinterpret_cast<uint4*>(p) = u; }
     __device__ void decode(float (&v)[8]) const { InTraits<__nv_bfloat16>::decode(u, v); }
     __device__ void encode(const float (&v)[8])
     {
@@ -68,8 +90,8 @@ template <> struct Vec8<__nv_bfloat16> {
 };
 template <> struct Vec8<__half> {
     uint4 u;
-    __device__ void load(const __half* p) { u = load16(p); }
-    __device__ void store(__half* p) const { *reinterpret_cast<uint4*>(p) = u; }
+    __device__ void load(const __half* p, bool) { u = load16(p); }
+    __device__ void store(__half* p, bool) const { *reinterpret_cast<uint4*>(p) = u; }
     __device__ void decode(float (&v)[8]) const
     {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -87,26 +109,24 @@ template <> struct Vec8<__half> {
 };
 
 template <typename T>
-__device__ __forceinline__ void store_as(void* out, int64_t idx, const float (&v)[8])
+__device__ __forceinline__ void store_as(void* out, int64_t idx, const float (&v)[8], bool wide)
 {
     Vec8<T> w;
     w.encode(v);
-    w.store(static_cast<T*>(out) + idx);
+    w.store(static_cast<T*>(out) + idx, wide);
 }
 
-__device__ __forceinline__ void load_weights(const float* p, float (&v)[8])
+__device__ __forceinline__ void load_weights(const float* p, float (&v)[8], bool wide)
 {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-__device__ __forceinline__ void multiply(float (&z)[8], const float* weights)
-{
-    float w[8];
-    load_weights(weights, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] *= w[i];
+    if (wide) {
+        asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+            : "l"(p));
+    } else {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
 }
 
 // Sum over the TPR threads of a row, in a fixed order. `red` holds two slots of TPR / 32 floats,
@@ -116,7 +136,7 @@ template <int TPR>
 __device__ __forceinline__ float row_sum(float s, float* red, int& slot)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if constexpr (TPR > 32) {
         constexpr int W = TPR / 32;
         float* mine = red + slot * W;
@@ -161,17 +181,36 @@ __device__ __forceinline__ void normalise(const NormLaunch& a, float (&z)[V][8],
         for (int i = 0; i < 8; ++i) z[k][i] *= rstd;
 }
 
-// One row per TPR threads; thread t holds the row's 8-element vectors t, t + TPR, ... (V of them).
-template <typename T, int TPR, int V, bool QUANT>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(const NormLaunch a)
+// z *= weights of its columns
+template <int TPR, int V>
+__device__ __forceinline__ void multiply(float (&z)[V][8], const bool (&in)[V], int t, const float* weights, bool wide)
 {
-    __shared__ float red[2 * (TPR / 32)];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        if (!in[k]) continue;
+        float w[8];
+        load_weights(weights + 8 * (t + k * TPR), w, wide);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[k][i] *= w[i];
+    }
+}
+
+// One row per TPR threads; thread t holds the row's 8-element vectors t, t + TPR, ... (V of them).
+// What bounds it: HBM without post_weight and gate (16384 x 6144 bf16: 122 us, 6.6 TB/s); with
+// them (140 us) the second chain of sum and barrier, and the fp32 weights, which pass L1 for
+// every row. Two rows to a block share the weights but keep fewer rows on an SM (160 us); so do
+// blocks that walk several rows with the next row's loads ahead (138 us where this takes 122).
+template <typename T, int TPR, int V, bool QUANT>
+__global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) residual_norm_kernel(const NormLaunch a)
+{
+    __shared__ float red[TPR > 32 ? 2 * (TPR / 32) : 1];
     const int t = threadIdx.x % TPR;
-    const int64_t row = TPR == 32 ? blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+    const int64_t row = TPR <= 32 ? blockIdx.x * static_cast<int64_t>(blockDim.x / TPR) + threadIdx.x / TPR : blockIdx.x;
     grid_dependency_wait();
     grid_launch_dependents();
-    if (row >= a.rows) return;                       // whole warps, and only where TPR == 32
-    const int nvec = a.H >> 3;
+    // rows past the last one (TPR <= 32) hold nothing, but stay for their warp's exchanges
+    const int nvec = row < a.rows ? a.H >> 3 : 0;
+    const bool wide = a.wide != 0;
     int slot = 0;
     bool in[V];
     Vec8<T> xw[V], yw[V];
@@ -184,8 +223,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(co
         xw[k] = Vec8<T>{};
         yw[k] = Vec8<T>{};
         if (in[k]) {
-            xw[k].load(x + 8 * c);
-            if (a.y) yw[k].load(y + 8 * c);
+            xw[k].load(x + 8 * c, wide);
+            if (a.y) yw[k].load(y + 8 * c, wide);
         }
     }
     float z[V][8];
@@ -194,22 +233,20 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(co
         for (int k = 0; k < V; ++k) yw[k].decode(z[k]);
         if (a.post) {
             normalise<TPR, V>(a, z, in, red, slot);
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                if (in[k]) multiply(z[k], a.post + 8 * (t + k * TPR));
+            multiply<TPR, V>(z, in, t, a.post, wide);
         }
+        if (a.gate) multiply<TPR, V>(z, in, t, a.gate, wide);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             if (!in[k]) continue;
             float xv[8];
             xw[k].decode(xv);
-            if (a.gate) multiply(z[k], a.gate + 8 * (t + k * TPR));
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[k][i] = fmaf(a.scale, z[k][i], xv[i]);
             // the next norm is of the residual as it is stored: what a separate norm would read
             xw[k].encode(z[k]);
             xw[k].decode(z[k]);
-            if (a.r) xw[k].store(static_cast<T*>(a.r) + row * a.ld_r + 8 * (t + k * TPR));
+            if (a.r) xw[k].store(static_cast<T*>(a.r) + row * a.ld_r + 8 * (t + k * TPR), wide);
         }
     } else {
 #pragma unroll
@@ -221,22 +258,24 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(co
     for (int k = 0; k < V; ++k) {
         const int c = t + k * TPR;
         if (in[k]) {
+            float w[8];
+            load_weights(a.w + 8 * c, w, wide);
             if (a.b) {
-                float w[8], b[8];
-                load_weights(a.w + 8 * c, w);
-                load_weights(a.b + 8 * c, b);
+                float b[8];
+                load_weights(a.b + 8 * c, b, wide);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) z[k][i] = fmaf(z[k][i], w[i], b[i]);
             } else {
-                multiply(z[k], a.w + 8 * c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[k][i] *= w[i];
             }
         }
         if constexpr (!QUANT) {
             if (!in[k]) continue;
             const int64_t idx = row * a.H + 8 * c;
-            if (a.out_dt == 2) store_as<float>(a.out, idx, z[k]);
-            else if (a.out_dt == 1) store_as<__half>(a.out, idx, z[k]);
-            else store_as<__nv_bfloat16>(a.out, idx, z[k]);
+            if (a.out_dt == 2) store_as<float>(a.out, idx, z[k], wide);
+            else if (a.out_dt == 1) store_as<__half>(a.out, idx, z[k], wide);
+            else store_as<__nv_bfloat16>(a.out, idx, z[k], wide);
         } else {
             // lanes 2 j, 2 j + 1 share a 16-element block, lanes 8 j .. 8 j + 7 a tiled 4-scale word
             float amax = 0.0f;
@@ -263,12 +302,13 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(co
 template <typename T, int TPR, int V>
 cudaError_t launch(const NormLaunch& a, cudaStream_t stream)
 {
-    // rows of one warp: four to a block once that still leaves every SM a block
-    const int rpb = TPR == 32 && a.rows >= 1024 ? 4 : 1;
+    // rows of a warp or less: four warps to a block once that still leaves every SM a block
+    const int threads = TPR > 32 ? TPR : a.rows * TPR >= 32 * 1024 ? 128 : 32;
+    const int64_t per_block = TPR > 32 ? 1 : threads / TPR;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(TPR * rpb), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>((a.rows + per_block - 1) / per_block), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -282,30 +322,48 @@ cudaError_t launch(const NormLaunch& a, cudaStream_t stream)
 template <typename T, int TPR>
 cudaError_t launch_v(const NormLaunch& a, cudaStream_t stream)
 {
-    switch ((a.H / 8 + TPR - 1) / TPR) {
-        case 1: return launch<T, TPR, 1>(a, stream);
-        case 2: return launch<T, TPR, 2>(a, stream);
-        case 3: return launch<T, TPR, 3>(a, stream);
-        case 4: return launch<T, TPR, 4>(a, stream);
-        default: return cudaErrorInvalidValue;
+    if constexpr (TPR < 32) {
+        return launch<T, TPR, 1>(a, stream);
+    } else {
+        switch ((a.H / 8 + TPR - 1) / TPR) {
+            case 1: return launch<T, TPR, 1>(a, stream);
+            case 2: return launch<T, TPR, 2>(a, stream);
+            case 3: return launch<T, TPR, 3>(a, stream);
+            case 4: return launch<T, TPR, 4>(a, stream);
+            default: return cudaErrorInvalidValue;
+        }
     }
 }
 
 template <typename T>
 cudaError_t launch_t(const NormLaunch& a, cudaStream_t stream, int num_sms)
 {
-    // Threads per row: as few as hold the row (32 up to H = 1024, 256 up to 8192, 1024 up to
-    // 32768); with no more rows than SMs the row is spread wider, one vector per thread.
-    const bool few = a.rows <= num_sms;
-    if (a.H <= (few ? 256 : 1024)) return launch_v<T, 32>(a, stream);
-    if (a.H <= (few ? 2048 : 8192)) return launch_v<T, 256>(a, stream);
+    // Threads per row: as few as hold the row in four vectors each (16384 x 6144 bf16 with post_weight
+    // and gate on 256 threads 139 us, on 512 160), two of fp32 (16384 x 8192 on 512 threads 315 us,
+    // on 256 344); with no more rows than SMs the row is spread wider, one vector per thread.
+    const int64_t v = a.rows <= num_sms ? 1 : sizeof(T) == 4 ? 2 : 4;
+    if (a.H <= 64) return launch_v<T, 8>(a, stream);
+    if (a.H <= 128) return launch_v<T, 16>(a, stream);
+    if (a.H <= 256 * v) return launch_v<T, 32>(a, stream);
+    if (a.H <= 2048 * v) return launch_v<T, 256>(a, stream);
+    if (a.H <= 4096 * v) return launch_v<T, 512>(a, stream);
     return launch_v<T, 1024>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_residual_norm(const NormLaunch& a, cudaStream_t stream, int num_sms)
+cudaError_t launch_residual_norm(const NormLaunch& args, cudaStream_t stream, int num_sms)
 {
+    // every fp32 access 32-byte aligned: the weights, and the rows of fp32 tensors
+    NormLaunch a = args;
+    uintptr_t all = reinterpret_cast<uintptr_t>(a.w) | reinterpret_cast<uintptr_t>(a.b) |
+                    reinterpret_cast<uintptr_t>(a.post) | reinterpret_cast<uintptr_t>(a.gate);
+    if (a.dtype == 2)
+        all |= reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.r) |
+               static_cast<uintptr_t>(a.ld_x * 4) | static_cast<uintptr_t>(a.y ? a.ld_y * 4 : 0) |
+               static_cast<uintptr_t>(a.r ? a.ld_r * 4 : 0);
+    if (!a.q && a.out_dt == 2) all |= reinterpret_cast<uintptr_t>(a.out);
+    a.wide = (all & 31u) == 0 ? 1 : 0;
     switch (a.dtype) {
         case 0: return launch_t<__nv_bfloat16>(a, stream, num_sms);
         case 1: return launch_t<__half>(a, stream, num_sms);

@@ -17,7 +17,7 @@ from test_fused_products_gpu import check_quantised
 pytestmark = pytest.mark.gpu
 
 EPS = 1e-5
-SHAPES = [(1, 8), (3, 16), (5, 264), (1030, 520), (200, 1024), (40, 1032), (150, 2048), (149, 4096), (33, 6144),
+SHAPES = [(1, 8), (3, 16), (77, 64), (1025, 128), (4099, 104), (5, 264), (1030, 520), (200, 1024), (40, 1032), (150, 2048), (149, 4096), (33, 6144),
           (300, 6144), (300, 8192), (4, 8200), (160, 12288), (2, 32768), (200, 24576)]
 
 
@@ -103,7 +103,7 @@ def test_norm_alone(cuda_device, T, H):
         check(out, want, stored(want, e, dtype), str(dtype))
 
 
-@pytest.mark.parametrize("T,H", [(1, 64), (3, 16), (5, 272), (1030, 576), (129, 1024), (150, 2048), (33, 6144), (300, 6144),
+@pytest.mark.parametrize("T,H", [(1, 64), (3, 16), (77, 64), (19, 48), (4099, 128), (5, 272), (1030, 576), (129, 1024), (150, 2048), (33, 6144), (300, 6144),
                                  (4, 8256), (160, 12288), (2, 32768)])
 def test_quantised(cuda_device, T, H):
     d = cuda_device
@@ -156,6 +156,21 @@ def test_rows_of_a_wider_array_and_in_place(cuda_device):
             y4 = c.y.clone()
             o4, _ = nv.residual_norm(c.x, c.w, y4, r_out=y4, **c.kw)
             assert torch.equal(o3, out) and torch.equal(x3, r) and torch.equal(o4, out) and torch.equal(y4, r)
+
+
+def test_fp32_pointers_aligned_to_16_bytes_only(cuda_device):
+    """Weights and fp32 rows on 16- but not 32-byte addresses give the bits of aligned ones."""
+    d = cuda_device
+    shift = lambda t: torch.cat([t.new_zeros(4), t.flatten()])[4:].view(t.shape)  # noqa: E731
+    for dtype in DTYPES:
+        c = Case(d, 33, 1024, dtype, "layer", post=True, gate=True, bias=True)
+        out, r = c.run(torch.float32)
+        kw = dict(c.kw, bias=shift(c.kw["bias"]), post_weight=shift(c.kw["post_weight"]), gate=shift(c.kw["gate"]))
+        w = shift(c.w)
+        assert w.data_ptr() % 32 == 16
+        x, y = (shift(c.x), shift(c.y)) if dtype == torch.float32 else (c.x, c.y)
+        o2, r2 = nv.residual_norm(x, w, y, out=shift(torch.empty_like(out)), r_out=shift(torch.empty_like(r)) if dtype == torch.float32 else None, **kw)
+        assert torch.equal(o2, out) and torch.equal(r2, r)
 
 
 def test_large_mean_and_constant_rows(cuda_device):
