@@ -195,12 +195,16 @@ __device__ __forceinline__ float2 unpack_out16x2(uint32_t w, int32_t dt)
 }
 
 // The side input (residual or dh) holds out_dtype elements and may be the output itself, so it
-// is read with plain loads, each element by the thread that later writes its place.
-__device__ __forceinline__ float load_side1(const GemmArgs& a, size_t idx)
+// is read with plain loads, each element by the thread that later writes its place, or whose
+// value goes into the store that does. An element as it sits in memory, and its value:
+__device__ __forceinline__ uint32_t load_side_bits(const GemmArgs& a, size_t idx)
 {
-    if (a.out_dtype == kOutF32) return static_cast<const float*>(a.side)[idx];
-    const uint32_t w = static_cast<const uint16_t*>(a.side)[idx];
-    return unpack_out16x2(w, a.out_dtype).x;
+    if (a.out_dtype == kOutF32) return static_cast<const uint32_t*>(a.side)[idx];
+    return static_cast<const uint16_t*>(a.side)[idx];
+}
+__device__ __forceinline__ float side_value(const GemmArgs& a, uint32_t bits)
+{
+    return a.out_dtype == kOutF32 ? __uint_as_float(bits) : unpack_out16x2(bits, a.out_dtype).x;
 }
 
 // N consecutive side elements from idx (idx % N == 0, N = 4 or 8).
@@ -274,84 +278,10 @@ __device__ __forceinline__ void linear_act(const float* bias, int32_t act, float
     act_apply(v, act);
 }
 
-// Swap tiles: the lane's output column n = p0 + 32 quad + lane, tokens c .. c + 15.
-template <class Cfg>
-__device__ __forceinline__ void linear_tok16(const GemmArgs& a, const Tile& ti, int quad, int lane, int c,
-                                             const uint32_t (&r)[16], float alpha)
-{
-    const int n = ti.p0 + 32 * quad + lane;
-    const float b = a.bias != nullptr && n < a.N ? __ldg(a.bias + n) : 0.0f;
-    float v[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = fmaf(alpha, __uint_as_float(r[j]), b);
-    act_apply(v, a.act_fn);
-    if (a.side != nullptr) {
-        float s[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int m = ti.q0 + c + j;
-            s[j] = m < a.M && n < a.N ? load_side1(a, static_cast<size_t>(m) * a.N + n) : 0.0f;
-        }
-        // (the 16-bit stores below go to other columns than this lane's: every lane has its
-        // residuals before any lane of the warp stores, and no other warp has these columns)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = fmaf(a.side_scale, s[j], v[j]);
-        __syncwarp();
-    }
-    uint32_t o[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(v[j]);
-    if (a.out_dtype != kOutF32) store_tok16<Cfg>(a, ti, quad, lane, c, o, 1.0f);
-    else store_out16<Cfg>(a, ti, n, c, o, 1.0f);
-}
+// ------------------------------------------------------------------ few tokens (weights as the MMA M operand)
 
-// A reduced split-K chunk (see store_chunk): eight consecutive outputs per item.
-template <class Cfg>
-__device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& ti, const float* src, int nsrc, int r0,
-                                             int rows, int tid, float alpha)
-{
-    constexpr int BN = Cfg::BN;
-    constexpr int PS = Cfg::PSTRIDE;
-    const int G = Cfg::SWAP ? rows >> 3 : BN / 8;
-    const int items = Cfg::SWAP ? BN * G : rows * G;
-    for (int item = tid; item < items; item += 128) {
-        const int outer = item / G, inner = (item - outer * G) * 8;
-        // swap: outer = token column, inner = chunk row; otherwise outer = chunk row, inner = column
-        const int m = Cfg::SWAP ? ti.q0 + outer : ti.p0 + r0 + outer;
-        const int n0 = Cfg::SWAP ? ti.p0 + r0 + inner : ti.q0 + inner;
-        if (m >= a.M || n0 >= a.N) continue;
-        const size_t idx = static_cast<size_t>(m) * a.N + n0;
-        float s[8];
-        if (a.side != nullptr) load_side(a, idx, s);          // in flight during the sums
-        float v[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = 0.0f;
-        for (int j = 0; j < nsrc; ++j) {
-            if constexpr (Cfg::SWAP) {
-                const float* p = src + (j * rows + inner) * PS + outer;
-#pragma unroll
-                for (int t = 0; t < 8; ++t) v[t] += p[t * PS];
-            } else {
-                const float* p = src + (j * rows + outer) * PS + inner;
-#pragma unroll
-                for (int t = 0; t < 8; t += 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(p + t);
-                    v[t] += x.x; v[t + 1] += x.y; v[t + 2] += x.z; v[t + 3] += x.w;
-                }
-            }
-        }
-        linear_act(a.bias != nullptr ? a.bias + n0 : nullptr, a.act_fn, alpha, v);
-        if (a.side != nullptr) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t) v[t] = fmaf(a.side_scale, s[t], v[t]);
-        }
-        store_out8(a, idx, v);
-    }
-}
-
-// ------------------------------------------------------------------ gated product
-
-// One value of h (index j of token m), alone or with its half-warp's block.
+// One value of h (index j of token m), alone or with its block: the 16 lanes of a half-warp hold
+// the 16 indices of one block of the same token. `ok`: the token exists. All lanes take part.
 template <class Cfg>
 __device__ __forceinline__ void glu_put(const GemmArgs& a, int m, int j, float h, bool ok)
 {
@@ -362,31 +292,30 @@ __device__ __forceinline__ void glu_put(const GemmArgs& a, int m, int j, float h
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const uint32_t sf = block_scale(amax, __ldg(a.gs_h), rcp);
-        const uint32_t code = f32x2_to_e2m1x2(__fmul_rn(h, rcp), 0.0f) & 0xFu;
-        const uint32_t next = __shfl_xor_sync(0xffffffffu, code, 1);
-        if (ok && (j & 1) == 0)
-            a.h_q[static_cast<int64_t>(m) * (a.inter >> 1) + (j >> 1)] = static_cast<uint8_t>(code | (next << 4));
+        // eight lanes' codes as one word
+        uint32_t w = (f32x2_to_e2m1x2(__fmul_rn(h, rcp), 0.0f) & 0xFu) << (4 * (j & 7));
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+        if (ok && (j & 7) == 0)
+            *reinterpret_cast<uint32_t*>(a.h_q + static_cast<int64_t>(m) * (a.inter >> 1) + (j >> 1)) = w;
         if (ok && (j & 15) == 0) *h_sf_at(a, m, j >> 4) = static_cast<uint8_t>(sf);
     }
 }
 
-// (g, u) pairs of h index j of N tokens m[], after the reduction; the 16 lanes of a half-warp hold
-// the 16 indices of one block of the same token. `ok`: the token exists. All lanes take part.
+// (g, u) pairs of h index j of the N tokens m[], with their dh (kEpiGluGrad).
 template <class Cfg, int N>
 __device__ __forceinline__ void glu_lane(const GemmArgs& a, const int (&m)[N], int j, float (&g)[N], const float (&u)[N],
-                                         const bool (&ok)[N])
+                                         const bool (&ok)[N], const float (&dh)[N])
 {
     if constexpr (Cfg::EPI == kEpiGluGrad) {
-        float d[N], s[N];
-#pragma unroll
-        for (int t = 0; t < N; ++t) s[t] = ok[t] ? load_side1(a, static_cast<size_t>(m[t]) * a.inter + j) : 0.0f;
+        float d[N];
         act_apply_grad(g, d, a.act_fn);
 #pragma unroll
         for (int t = 0; t < N; ++t) {
             if (!ok[t]) continue;
             const size_t idx = static_cast<size_t>(m[t]) * a.N + j;
-            store_out1(a, idx, s[t] * u[t] * d[t]);
-            store_out1(a, idx + a.inter, s[t] * g[t]);
+            store_out1(a, idx, dh[t] * u[t] * d[t]);
+            store_out1(a, idx + a.inter, dh[t] * g[t]);
         }
     } else {
         act_apply(g, a.act_fn);
@@ -395,117 +324,356 @@ __device__ __forceinline__ void glu_lane(const GemmArgs& a, const int (&m)[N], i
     }
 }
 
-// Weight-major tiles: lanes 0-15 hold 16 gate rows and lanes 16-31 their up rows, for tokens
-// c .. c + 15. One exchange gives lane i (i < 16) both halves of tokens c .. c + 7 and lane
-// 16 + i those of tokens c + 8 .. c + 15.
+// A warp's part of a swap tile without split-K: 32 weight rows (lane = row) x at most 32 tokens,
+// taken in 16s. Linear: lane = output column n. Gated: lanes 0-15 hold 16 gate rows and lanes
+// 16-31 their up rows; one exchange gives lane i (i < 16) both halves of tokens c .. c + 7 and
+// lane 16 + i those of tokens c + 8 .. c + 15. The residual or dh elements are requested before
+// the accumulator is awaited.
 template <class Cfg>
-__device__ __forceinline__ void glu_tok16(const GemmArgs& a, const Tile& ti, int quad, int lane, int c,
-                                          const uint32_t (&r)[16], float alpha)
-{
-    const int j0 = (ti.p0 >> 1) + 16 * quad;
-    if (j0 >= a.inter) return;                       // warp-uniform
-    const bool up = lane >= 16;
-    int m[8];
-    float g[8], u[8];
-    bool ok[8];
-#pragma unroll
-    for (int cc = 0; cc < 8; ++cc) {
-        const float lo = alpha * __uint_as_float(r[cc]);        // token c + cc
-        const float hi = alpha * __uint_as_float(r[cc + 8]);    // token c + 8 + cc
-        const float other = __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16);
-        m[cc] = ti.q0 + c + cc + (up ? 8 : 0);
-        ok[cc] = m[cc] < a.M;
-        g[cc] = up ? other : lo;
-        u[cc] = up ? hi : other;
-    }
-    glu_lane<Cfg>(a, m, j0 + (lane & 15), g, u, ok);
-}
+struct EpiToks {
+    static constexpr bool LINEAR = Cfg::EPI == kEpiLinear;
+    static constexpr bool GRAD = Cfg::EPI == kEpiGluGrad;
+    static constexpr int NT = Cfg::BN == 64 ? 32 : 16;          // tokens per warp
+    const GemmArgs& a;
+    const int quad, lane;
+    uint32_t side[LINEAR ? NT : GRAD ? NT / 2 : 1];
+    float bias = 0.0f;
 
-// A reduced split-K chunk. Weight-major: item = (32-row group, token, index of the group), so that
-// a half-warp has one block of one token. Token-major: item = (chunk row, four indices of h); the
-// four lanes of a block are neighbours. The item count is a multiple of 128 either way: every
-// lane of a warp stays in the loop for its exchanges.
-template <class Cfg>
-__device__ __forceinline__ void glu_chunk(const GemmArgs& a, const Tile& ti, const float* src, int nsrc, int r0,
-                                          int rows, int tid, float alpha)
-{
-    constexpr int BN = Cfg::BN;
-    constexpr int PS = Cfg::PSTRIDE;
-    if constexpr (Cfg::SWAP) {
-        // two tokens per item: c and c + BN / 2
-        for (int item = tid; item < (rows >> 5) * (BN / 2) * 16; item += 128) {
-            const int i = item & 15, c = (item >> 4) % (BN / 2), unit = (item >> 4) / (BN / 2);
-            const float* p = src + (32 * unit + i) * PS + c;
-            float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
-            for (int k = 0; k < nsrc; ++k) {
+    __device__ __forceinline__ EpiToks(const GemmArgs& args, int q, int l) : a(args), quad(q), lane(l) {}
+
+    // token of element i of this lane's list, in 16-token group h that starts at column c
+    __device__ __forceinline__ int token(const Tile& ti, int c, int i) const
+    {
+        return ti.q0 + c + (LINEAR ? i : i + (lane >= 16 ? 8 : 0));
+    }
+
+    __device__ __forceinline__ void begin(const Tile& ti, int half)
+    {
+        const int c_lo = half ? (Cfg::BN == 16 ? 16 : Cfg::BN / 2) : 0;
+        if (c_lo >= Cfg::BN) return;
+        if constexpr (LINEAR) {
+            const int n = ti.p0 + 32 * quad + lane;
+            if (a.bias != nullptr && n < a.N) bias = __ldg(a.bias + n);
+            if (a.side != nullptr) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    g[t] += p[k * rows * PS + t * (BN / 2)];
-                    u[t] += p[(k * rows + 16) * PS + t * (BN / 2)];
+                for (int i = 0; i < NT; ++i) {
+                    const int m = token(ti, c_lo, i);
+                    side[i] = m < a.M && n < a.N ? load_side_bits(a, static_cast<size_t>(m) * a.N + n) : 0u;
                 }
             }
-            const int j = ((ti.p0 + r0) >> 1) + 16 * unit + i;
-            int m[2];
-            bool ok[2];
+        } else if constexpr (GRAD) {
+            const int j = (ti.p0 >> 1) + 16 * quad + (lane & 15);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                g[t] *= alpha;
-                u[t] *= alpha;
-                m[t] = ti.q0 + c + t * (BN / 2);
-                ok[t] = m[t] < a.M && j < a.inter;
+            for (int i = 0; i < NT / 2; ++i) {
+                const int m = token(ti, c_lo + 16 * (i >> 3), i & 7);
+                side[i] = m < a.M && j < a.inter ? load_side_bits(a, static_cast<size_t>(m) * a.inter + j) : 0u;
             }
-            glu_lane<Cfg>(a, m, j, g, u, ok);
         }
-    } else {
-        constexpr int G = BN / 8;                    // items per row: four indices of h each
-        static_assert(G % 4 == 0 && G * 8 % 128 == 0, "whole warps of items (chunks are multiples of 8 rows)");
-        for (int item = tid; item < rows * G; item += 128) {
-            const int lr = item / G, cg = (item % G) >> 2, s = item & 3;
-            const float* p = src + lr * PS + 32 * cg + 4 * s;
-            float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int k = 0; k < nsrc; ++k) {
-                const float4 x = *reinterpret_cast<const float4*>(p + k * rows * PS);
-                const float4 y = *reinterpret_cast<const float4*>(p + k * rows * PS + 16);
-                g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
-                u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+    }
+
+    // Tokens c .. c + 15, the h-th sixteen of the warp (h is 0 or 1, known at compile time).
+    __device__ __forceinline__ void run(const Tile& ti, int h, int c, const uint32_t (&r)[16], float alpha)
+    {
+        if constexpr (LINEAR) {
+            const int n = ti.p0 + 32 * quad + lane;
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = fmaf(alpha, __uint_as_float(r[j]), bias);
+            act_apply(v, a.act_fn);
+            if (a.side != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = fmaf(a.side_scale, side_value(a, side[(NT == 32 ? 16 * h : 0) + j]), v[j]);
             }
+            uint32_t o[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) { g[i] *= alpha; u[i] *= alpha; }
-            const int m = ti.p0 + r0 + lr, j = ((ti.q0 + 32 * cg) >> 1) + 4 * s;
-            const bool ok = m < a.M && j < a.inter;
-            if constexpr (Cfg::EPI == kEpiGluGrad) {
-                float d[4], dh[4];
-                if (!ok) continue;                   // no exchange below
-                load_side(a, static_cast<size_t>(m) * a.inter + j, dh);
-                act_apply_grad(g, d, a.act_fn);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(v[j]);
+            if (a.out_dtype != kOutF32) store_tok16<Cfg>(a, ti, quad, lane, c, o, 1.0f);
+            else store_out16<Cfg>(a, ti, n, c, o, 1.0f);
+        } else {
+            const int j0 = (ti.p0 >> 1) + 16 * quad;
+            if (j0 >= a.inter) return;               // warp-uniform
+            const bool up = lane >= 16;
+            int m[8];
+            float g[8], u[8];
+            bool ok[8];
+            float s[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) { d[i] = dh[i] * u[i] * d[i]; g[i] = dh[i] * g[i]; }
-                const size_t idx = static_cast<size_t>(m) * a.N + j;
-                store_out4(a, idx, d);
-                store_out4(a, idx + a.inter, g);
+            for (int i = 0; i < 8; ++i) {
+                const float lo = alpha * __uint_as_float(r[i]);        // token c + i
+                const float hi = alpha * __uint_as_float(r[i + 8]);    // token c + 8 + i
+                const float other = __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16);
+                m[i] = token(ti, c, i);
+                ok[i] = m[i] < a.M;
+                g[i] = up ? other : lo;
+                u[i] = up ? hi : other;
+                s[i] = GRAD ? side_value(a, side[GRAD ? (NT == 32 ? 8 * h : 0) + i : 0]) : 0.0f;
+            }
+            glu_lane<Cfg>(a, m, j0 + (lane & 15), g, u, ok, s);
+        }
+    }
+};
+
+// ------------------------------------------------------------------ split-K
+
+// The split-K epilogue, by both epilogue warpgroups (256 threads; row: this thread's accumulator
+// row, half: its warpgroup). As in split_k_epilogue, the CTAs of a cluster hold consecutive K
+// slices of one tile, every slice's accumulator goes to the ranks that own its parts by st.async,
+// and each owner sums its parts over the ranks in order: deterministic. A part (chunk) is 8
+// accumulator rows; where a gated product's weights are those rows, one group of 16 gate and 16 up
+// rows for half of the tokens, so that every pair and block of h has one owner (8 such chunks of
+// 32 rows over at most 8 ranks). begin(), before the accumulator is awaited, works out where
+// everything goes (divisions by the cluster size) and requests the first residual or dh elements.
+template <class Cfg>
+struct EpiSplit {
+    static constexpr int BN = Cfg::BN;
+    static constexpr bool LINEAR = Cfg::EPI == kEpiLinear;
+    static constexpr bool GROUPS = Cfg::GLU && Cfg::SWAP;
+    static constexpr int CR = GROUPS ? 32 : 8;       // rows of a chunk
+    static constexpr int CW = GROUPS ? BN / 2 : BN;  // columns of a chunk
+    static constexpr int CHUNKS = GROUPS ? 8 : 16;
+    static constexpr int PS = CW + 4;
+    static constexpr int NT = GROUPS && BN >= 32 ? 2 : 1;        // tokens of a grouped item: c and c + CW / 2
+    static constexpr bool SIDE = LINEAR || Cfg::EPI == kEpiGluGrad;
+    static constexpr int SV = LINEAR ? 8 : GROUPS ? NT : 4;      // side elements of an item
+    struct Item { int m, j, src; bool ok; };         // token (row of the output), first column, offset of source 0
+
+    const GemmArgs& a;
+    const AbortState& ab;
+    uint64_t* const rx_bar;
+    float* const rx;
+    const int row, half, tid, cs;
+    // this row's (GROUPS: and token half's) place in its owner's receive buffer: a shared::cluster
+    // address and the owner's barrier, or here (dst 0)
+    float* mine[GROUPS ? 2 : 1];
+    uint32_t dst[GROUPS ? 2 : 1], bar[GROUPS ? 2 : 1];
+    int k0, n, items;                                // this rank's chunks [k0, k0 + n) and their items
+    Item item0;
+    float side0[SV];
+
+    __device__ __forceinline__ EpiSplit(const GemmArgs& args, uint8_t* smem, uint64_t* rxb, int r, int h,
+                                        const AbortState& abort)
+        : a(args), ab(abort), rx_bar(rxb), rx(reinterpret_cast<float*>(smem + (Cfg::RX_OWN ? Cfg::OFF_RX : Cfg::OFF_P))),
+          row(r), half(h), tid(128 * h + r), cs(args.cluster_size)
+    {
+    }
+
+    __device__ __forceinline__ int first(int r) const { return (r * CHUNKS + cs - 1) / cs; }
+
+    __device__ __forceinline__ void begin(const Tile& ti)
+    {
+        const int rank = static_cast<int>(cluster_ctarank());
+        k0 = first(rank);
+        n = first(rank + 1) - k0;
+        items = GROUPS ? n * 16 * (CW / NT) : Cfg::SWAP ? n * BN : n * CR * (BN / 8);
+#pragma unroll
+        for (int p = 0; p < (GROUPS ? 2 : 1); ++p) {
+            const int chunk = GROUPS ? 2 * (row >> 5) + p : row >> 3;
+            const int owner = chunk * cs / CHUNKS;
+            const int o0 = first(owner), on = first(owner + 1) - o0;
+            mine[p] = rx + ((rank * on + chunk - o0) * CR + (row & (CR - 1))) * PS;
+            dst[p] = owner == rank ? 0u : mapa_shared(smem_u32(mine[p]), static_cast<uint32_t>(owner));
+            bar[p] = owner == rank ? 0u : mapa_shared(smem_u32(rx_bar), static_cast<uint32_t>(owner));
+        }
+        if constexpr (SIDE) item0 = item_of(ti, tid);
+        if constexpr (SIDE) {
+            if (a.side != nullptr && tid < items) load_item_side(item0, side0);
+        }
+    }
+
+    __device__ __forceinline__ Item item_of(const Tile& ti, int item) const
+    {
+        Item it;
+        if constexpr (GROUPS) {
+            // (index of the group, token, chunk): a half-warp holds one block of one token
+            const int i = item & 15, c = (item >> 4) % (CW / NT), k = (item >> 4) / (CW / NT);
+            const int chunk = k0 + k;
+            it.m = ti.q0 + (chunk & 1) * CW + c;
+            it.j = (ti.p0 >> 1) + 16 * (chunk >> 1) + i;
+            it.src = (k * CR + i) * PS + c;
+            it.ok = it.m < a.M && it.j < a.inter;
+        } else if constexpr (Cfg::SWAP) {
+            // (chunk, token): eight output columns, neighbouring chunks by neighbouring threads
+            const int c = item / n, k = item - c * n;
+            it.m = ti.q0 + c;
+            it.j = ti.p0 + 8 * (k0 + k);
+            it.src = k * CR * PS + c;
+            it.ok = it.m < a.M && it.j < a.N;
+        } else {
+            // (column group, chunk row): eight output columns, or four indices of h
+            const int g = item % (BN / 8), r = item / (BN / 8);
+            it.m = ti.p0 + 8 * k0 + r;
+            if constexpr (LINEAR) {
+                it.j = ti.q0 + 8 * g;
+                it.src = r * PS + 8 * g;
+                it.ok = it.m < a.M && it.j < a.N;
             } else {
-                act_apply(g, a.act_fn);
+                it.j = ((ti.q0 + 32 * (g >> 2)) >> 1) + 4 * (g & 3);
+                it.src = r * PS + 32 * (g >> 2) + 4 * (g & 3);
+                it.ok = it.m < a.M && it.j < a.inter;
+            }
+        }
+        return it;
+    }
+
+    __device__ __forceinline__ void load_item_side(const Item& it, float (&s)[SV]) const
+    {
+        const int64_t ld = LINEAR ? a.N : a.inter;
+        if constexpr (GROUPS) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) g[i] *= u[i];
-                if constexpr (Cfg::EPI == kEpiGlu) {
-                    if (ok) store_out4(a, static_cast<size_t>(m) * a.inter + j, g);
+            for (int t = 0; t < NT; ++t)
+                s[t] = it.j < a.inter && it.m + t * (CW / 2) < a.M
+                           ? side_value(a, load_side_bits(a, (it.m + t * (CW / 2)) * ld + it.j)) : 0.0f;
+        } else {
+            if (it.ok) load_side(a, it.m * ld + it.j, s);
+        }
+    }
+
+    __device__ __forceinline__ void finish(const Tile& ti, uint32_t tacc, float alpha)
+    {
+        if (!Cfg::RX_OWN && cs > 1) { cluster_arrive(); cluster_wait(); }
+
+        // 1. this warpgroup's columns of its row to their owners
+        {
+            constexpr int SPAN = BN == 16 ? 16 : BN / 2;             // (16 columns: all by the first)
+            const int c_end = half * SPAN + SPAN < BN ? half * SPAN + SPAN : BN;
+            for (int c = half * SPAN; c < c_end; c += 16) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(tacc + c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // GROUPS: the token half of these four columns
+                    const int p = !GROUPS ? 0 : BN == 16 ? i >> 1 : half;
+                    const int cc = GROUPS ? (c + 4 * i) & (CW - 1) : c + 4 * i;
+                    const float4 f = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+                    const uint32_t d = GROUPS && p ? dst[GROUPS ? 1 : 0] : dst[0];
+                    if (d == 0u) *reinterpret_cast<float4*>((GROUPS && p ? mine[GROUPS ? 1 : 0] : mine[0]) + cc) = f;
+                    else st_async_f4(d + 4 * cc, f.x, f.y, f.z, f.w, GROUPS && p ? bar[GROUPS ? 1 : 0] : bar[0]);
+                }
+            }
+        }
+
+        // 2. wait (bounded) for the other ranks' parts; the barrier publishes this CTA's own
+        bool ok = true;
+        if (cs > 1) {
+            if (tid == 0) mbar_arrive_expect_tx(rx_bar, static_cast<uint32_t>((cs - 1) * n * CR * CW * 4));
+            ok = mbar_wait(rx_bar, 0, ab, kErrSplitRx);
+        }
+        __syncwarp();
+        ok = named_bar_and(2, 256, ok);
+        if (!ok) return;
+
+        // 3. sum over the ranks in order and finish. Item counts are multiples of 32 wherever lanes
+        // exchange values: whole warps stay in the loop.
+        const int step = n * CR * PS;                    // from one rank's copy to the next
+        for (int item = tid; item < items; item += 256) {
+            const Item it = SIDE && item == tid ? item0 : item_of(ti, item);
+            float s[SV];
+            if constexpr (SIDE) {
+                if (item == tid) {
+#pragma unroll
+                    for (int i = 0; i < SV; ++i) s[i] = side0[i];
+                } else if (a.side != nullptr) {
+                    load_item_side(it, s);
+                }
+            }
+            if constexpr (LINEAR) {
+                if (!it.ok) continue;
+                float v[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) v[t] = 0.0f;
+                for (int q = 0; q < cs; ++q) {
+                    const float* p = rx + q * step + it.src;
+                    if constexpr (Cfg::SWAP) {
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) v[t] += p[t * PS];
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < 8; t += 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(p + t);
+                            v[t] += x.x; v[t + 1] += x.y; v[t + 2] += x.z; v[t + 3] += x.w;
+                        }
+                    }
+                }
+                linear_act(a.bias != nullptr ? a.bias + it.j : nullptr, a.act_fn, alpha, v);
+                if (a.side != nullptr) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) v[t] = fmaf(a.side_scale, s[t], v[t]);
+                }
+                store_out8(a, static_cast<size_t>(it.m) * a.N + it.j, v);
+            } else if constexpr (GROUPS) {
+                float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};      // (two: the activations take pairs)
+                for (int q = 0; q < cs; ++q) {
+                    const float* p = rx + q * step + it.src;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        g[t] += p[t * (CW / 2)];
+                        u[t] += p[16 * PS + t * (CW / 2)];
+                    }
+                }
+                int m[2];
+                bool here[2];
+                float dh[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    g[t] *= alpha;
+                    u[t] *= alpha;
+                    m[t] = it.m + t * (CW / 2);
+                    here[t] = t < NT && m[t] < a.M && it.j < a.inter;
+                    if (SIDE && t < NT) dh[t] = s[t < SV ? t : 0];
+                }
+                if constexpr (NT == 2 || Cfg::EPI == kEpiGluGrad) {
+                    glu_lane<Cfg>(a, m, it.j, g, u, here, dh);
                 } else {
-                    float amax = fmaxf(fmaxf(fabsf(g[0]), fabsf(g[1])), fmaxf(fabsf(g[2]), fabsf(g[3]))), rcp;
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                    const uint32_t sf = block_scale(amax, __ldg(a.gs_h), rcp);
-                    const uint32_t q = f32x2_to_e2m1x2(__fmul_rn(g[0], rcp), __fmul_rn(g[1], rcp)) |
-                                       f32x2_to_e2m1x2(__fmul_rn(g[2], rcp), __fmul_rn(g[3], rcp)) << 8;
-                    if (ok) {
-                        *reinterpret_cast<uint16_t*>(a.h_q + static_cast<int64_t>(m) * (a.inter >> 1) + (j >> 1)) =
-                            static_cast<uint16_t>(q);
-                        if (s == 0) *h_sf_at(a, m, j >> 4) = static_cast<uint8_t>(sf);
+                    act_apply(g, a.act_fn);
+                    glu_put<Cfg>(a, m[0], it.j, g[0] * u[0], here[0]);
+                }
+            } else {
+                float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int q = 0; q < cs; ++q) {
+                    const float* p = rx + q * step + it.src;
+                    const float4 x = *reinterpret_cast<const float4*>(p);
+                    const float4 y = *reinterpret_cast<const float4*>(p + 16);
+                    g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
+                    u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) { g[i] *= alpha; u[i] *= alpha; }
+                if constexpr (Cfg::EPI == kEpiGluGrad) {
+                    if (!it.ok) continue;                // no exchange below
+                    float d[4];
+                    act_apply_grad(g, d, a.act_fn);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) { d[i] = s[i] * u[i] * d[i]; g[i] = s[i] * g[i]; }
+                    const size_t idx = static_cast<size_t>(it.m) * a.N + it.j;
+                    store_out4(a, idx, d);
+                    store_out4(a, idx + a.inter, g);
+                } else {
+                    act_apply(g, a.act_fn);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) g[i] *= u[i];
+                    if constexpr (Cfg::EPI == kEpiGlu) {
+                        if (it.ok) store_out4(a, static_cast<size_t>(it.m) * a.inter + it.j, g);
+                    } else {
+                        // the four lanes of a block are neighbours
+                        float amax = fmaxf(fmaxf(fabsf(g[0]), fabsf(g[1])), fmaxf(fabsf(g[2]), fabsf(g[3]))), rcp;
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                        const uint32_t sf = block_scale(amax, __ldg(a.gs_h), rcp);
+                        const uint32_t q = f32x2_to_e2m1x2(__fmul_rn(g[0], rcp), __fmul_rn(g[1], rcp)) |
+                                           f32x2_to_e2m1x2(__fmul_rn(g[2], rcp), __fmul_rn(g[3], rcp)) << 8;
+                        if (it.ok) {
+                            *reinterpret_cast<uint16_t*>(a.h_q + static_cast<int64_t>(it.m) * (a.inter >> 1) + (it.j >> 1)) =
+                                static_cast<uint16_t>(q);
+                            if ((it.j & 15) == 0) *h_sf_at(a, it.m, it.j >> 4) = static_cast<uint8_t>(sf);
+                        }
                     }
                 }
             }
         }
     }
-}
+};
 
 // ------------------------------------------------------------------ token-major tiles
 
@@ -904,23 +1072,5 @@ struct EpiRows {
         __syncwarp();
     }
 };
-
-// ------------------------------------------------------------------ dispatch (gemm_kernel.cuh)
-
-template <class Cfg>
-__device__ __forceinline__ void epi_tok16(const GemmArgs& a, const Tile& ti, int quad, int lane, int c,
-                                          const uint32_t (&r)[16], float alpha)
-{
-    if constexpr (Cfg::EPI == kEpiLinear) linear_tok16<Cfg>(a, ti, quad, lane, c, r, alpha);
-    else glu_tok16<Cfg>(a, ti, quad, lane, c, r, alpha);
-}
-
-template <class Cfg>
-__device__ __forceinline__ void epi_chunk(const GemmArgs& a, const Tile& ti, const float* src, int nsrc, int r0,
-                                          int rows, int tid, float alpha)
-{
-    if constexpr (Cfg::EPI == kEpiLinear) linear_chunk<Cfg>(a, ti, src, nsrc, r0, rows, tid, alpha);
-    else glu_chunk<Cfg>(a, ti, src, nsrc, r0, rows, tid, alpha);
-}
 
 }  // namespace nvfp4

@@ -232,16 +232,16 @@ struct GemmCfg {
     // and a 16-byte scale stage
     static constexpr int SWIGLU_BYTES = SWIGLU ? 1024 + kEpilogueWarps * (128 + 16) : 0;
     // split-K receive buffer: this rank's chunk (at most ceil(16 / cs) * 8 rows) from each of
-    // cs <= 8 ranks, cs * ceil(16 / cs) * 8 <= 168 rows of [BN + 4] floats; where weights are the
-    // MMA M operand of a GLU, whole 32-row (g, u) groups: cs * ceil(4 / cs) * 32 <= 256 rows.
-    // Few-token (swap)
+    // cs <= 8 ranks, cs * ceil(16 / cs) * 8 <= 168 rows of [BN + 4] floats (a GLU whose weights are
+    // the MMA M operand: see RX_FLOATS). Few-token (swap)
     // launches give it a region of its own (RX_OWN), so that the cluster barrier before the
     // exchange moves into the prologue; other split-K launches reuse the drained stage ring.
     static constexpr int PSTRIDE = BN + 4;
     static constexpr bool RX_OWN = SWAP && !GROUPED;
-    static constexpr int CHUNK_ROWS = GLU && SWAP ? 32 : 8;   // rows that stay together
-    static constexpr int RX_ROWS = CHUNK_ROWS == 32 ? 256 : 168;
-    static constexpr int RX_BYTES = RX_OWN ? ((RX_ROWS * PSTRIDE * 4 + 1023) & ~1023) : 0;
+    // (GLU and SWAP: 8 chunks of a 32-row (g, u) group and half of the tokens, cs * ceil(8 / cs) * 32
+    // <= 448 rows of [BN / 2 + 4] floats)
+    static constexpr int RX_FLOATS = GLU && SWAP ? 448 * (BN / 2 + 4) : 168 * PSTRIDE;
+    static constexpr int RX_BYTES = RX_OWN ? ((RX_FLOATS * 4 + 1023) & ~1023) : 0;
     // EPI_ROWS: per epilogue warp two 2 KB boxes (side input in, results out) and the bias of a
     // 64-column chunk. Costs 128-wide tiles one of their six ring stages; CTA pairs keep all five
     // (a fourth KB per warp would cost them one: 5-11% of 8192 x 6144 x 2048 and larger).
@@ -278,7 +278,7 @@ struct GemmCfg {
     static constexpr int OFF_EPI = (OFF_ACTQ + ACTQ_BYTES + 1023) & ~1023;
     static constexpr int SMEM_BYTES = OFF_EPI + EPI_BYTES + ALIGN_SLACK;
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
-    static_assert(RX_OWN || PAIR || RX_ROWS * PSTRIDE * 4 <= STAGES * STAGE_BYTES, "split-K receive buffer fits the pipeline buffers");
+    static_assert(RX_OWN || PAIR || RX_FLOATS * 4 <= STAGES * STAGE_BYTES, "split-K receive buffer fits the pipeline buffers");
     static_assert(OFF_Q % 1024 == 0 && OFF_SFP % 1024 == 0, "swizzle atoms need 1 KB alignment");
 };
 
@@ -604,21 +604,11 @@ __device__ __forceinline__ void store_rows64(const GemmArgs& a, const Tile& ti, 
     }
 }
 
-// Rows [chunk_begin(k), chunk_begin(k + 1)) of a 128-row tile belong to cluster rank k: whole
-// groups of CHUNK_ROWS rows, as evenly as possible (8-row groups: at most ceil(16 / cs) * 8 rows
-// per rank; 32-row groups: at most ceil(4 / cs) * 32, and some ranks of cs > 4 have none).
-template <class Cfg>
-__device__ __forceinline__ int chunk_begin(int k, int cs)
-{
-    constexpr int UNITS = 128 / Cfg::CHUNK_ROWS;
-    return ((k * UNITS + cs - 1) / cs) * Cfg::CHUNK_ROWS;
-}
+// Rows [chunk_begin(k), chunk_begin(k + 1)) of a 128-row tile belong to cluster rank k:
+// whole 8-row groups, as evenly as possible (at most ceil(16 / cs) * 8 rows per rank).
+__device__ __forceinline__ int chunk_begin(int k, int cs) { return ((k * 16 + cs - 1) / cs) * 8; }
 // The rank whose chunk holds `row`.
-template <class Cfg>
-__device__ __forceinline__ int chunk_owner(int row, int cs)
-{
-    return (row / Cfg::CHUNK_ROWS) * cs / (128 / Cfg::CHUNK_ROWS);
-}
+__device__ __forceinline__ int chunk_owner(int row, int cs) { return ((row >> 3) * cs) >> 4; }
 
 // Writes a reduced chunk of a tile: rows [r0, r0 + rows) of the 128 x BN accumulator tile,
 // each the in-order sum of `nsrc` fp32 copies in shared memory (copy j, chunk row lr, column
@@ -869,20 +859,23 @@ __device__ __forceinline__ float actq_quantize_t(const GemmArgs& a, uint8_t* sme
 
 // The fused epilogues (EPI), defined in gemm_epilogue.cuh, which every translation unit that
 // instantiates them includes. EpiRows: a warp's part of a non-swap tile (begin() requests what the
-// tile reads besides the accumulator, finish() drains it); epi_tok16: 16 columns (tokens) of a
-// warp's 32 weight rows (swap tiles); epi_chunk: a reduced split-K chunk, in the terms of
-// store_chunk.
+// tile reads besides the accumulator, finish() drains it); EpiToks: the same for a warp's part of a
+// swap tile; EpiSplit: the split-K epilogue.
 template <class Cfg>
 struct EpiRows;
 struct NoEpiRows {
     __device__ NoEpiRows(const GemmArgs&, const EpiMaps<false>&, int, int, int, uint8_t*, uint64_t*, const AbortState&) {}
 };
+struct NoEpiToks {
+    __device__ NoEpiToks(const GemmArgs&, int, int) {}
+};
+struct NoEpiSplit {
+    __device__ NoEpiSplit(const GemmArgs&, uint8_t*, uint64_t*, int, int, const AbortState&) {}
+};
 template <class Cfg>
-__device__ __forceinline__ void epi_tok16(const GemmArgs& a, const Tile& ti, int quad, int lane, int c,
-                                          const uint32_t (&r)[16], float alpha);
+struct EpiToks;
 template <class Cfg>
-__device__ __forceinline__ void epi_chunk(const GemmArgs& a, const Tile& ti, const float* src, int nsrc, int r0,
-                                          int rows, int tid, float alpha);
+struct EpiSplit;
 
 // Split-K epilogue of one CTA, run by the 128 threads of the first epilogue warpgroup
 // (thread = accumulator row; named barrier 2);
@@ -909,18 +902,18 @@ __device__ __forceinline__ void split_k_epilogue(const GemmArgs& a, const Tile& 
     const int cs = a.cluster_size;
     const int g = a.groups;
     const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int owner = chunk_owner<Cfg>(row, cs);
+    const int owner = chunk_owner(row, cs);
     float* rx = reinterpret_cast<float*>(smem + (Cfg::RX_OWN ? Cfg::OFF_RX : Cfg::OFF_P));
     // the receive buffer aliases the stage ring: wait until every CTA of the cluster has drained
     // its main loop (with a region of its own, the prologue's cluster barrier covered it)
     if (!Cfg::RX_OWN && cs > 1) { cluster_arrive(); cluster_wait(); }
 
-    const int my0 = chunk_begin<Cfg>(rank, cs);
-    const int my_rows = chunk_begin<Cfg>(rank + 1, cs) - my0;
+    const int my0 = chunk_begin(rank, cs);
+    const int my_rows = chunk_begin(rank + 1, cs) - my0;
     const int grp = ti.split / cs;
     const bool is_owner = owner == rank;
-    const int own0 = chunk_begin<Cfg>(owner, cs);
-    const int own_rows = chunk_begin<Cfg>(owner + 1, cs) - own0;
+    const int own0 = chunk_begin(owner, cs);
+    const int own_rows = chunk_begin(owner + 1, cs) - own0;
 
     // 1. every row to slot `rank` of its owner's receive buffer. tcgen05.ld is .sync.aligned:
     //    every lane of the warp executes every load, only the destination depends on the row.
@@ -945,7 +938,7 @@ __device__ __forceinline__ void split_k_epilogue(const GemmArgs& a, const Tile& 
     //    the named barrier publishes the own-slot rows to all 128 threads
     bool ok = true;
     if (cs > 1) {
-        if (row == 0)
+        if (row == my0)
             mbar_arrive_expect_tx(rx_bar, static_cast<uint32_t>((cs - 1) * my_rows * BN * 4));
         ok = mbar_wait(rx_bar, 0, ab, kErrSplitRx);
     }
@@ -954,10 +947,6 @@ __device__ __forceinline__ void split_k_epilogue(const GemmArgs& a, const Tile& 
     if (!ok) return;
 
     // 3. reduce over the ranks in order
-    if constexpr (Cfg::EPI != kEpiPlain) {       // never launched with a workspace (g == 1)
-        epi_chunk<Cfg>(a, ti, rx, cs, my0, my_rows, row, alpha);
-        return;
-    }
     if (g == 1) {
         store_chunk<Cfg>(a, ti, rx, cs, my0, my_rows, row, alpha);
         return;
@@ -1581,6 +1570,16 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
         if (Cfg::EPI_ROWS && tile_start < num_tiles) next = decode_tile<Cfg>(args, tile_start, s_prefix);
         for (int32_t t = tile_start; t < num_tiles; t += tile_step) {
             const Tile ti = Cfg::EPI_ROWS ? next : decode_tile<Cfg>(args, t, s_prefix);
+            std::conditional_t<Cfg::EPI != kEpiPlain && !Cfg::PAIR, EpiSplit<Cfg>, NoEpiSplit> split(args, smem, rx_bar, row,
+                                                                                                    half, ab);
+            if constexpr (Cfg::EPI != kEpiPlain && !Cfg::PAIR) {
+                if (args.splits > 1) split.begin(ti);
+            }
+            constexpr bool EPI_TOKS = Cfg::EPI != kEpiPlain && Cfg::SWAP;
+            std::conditional_t<EPI_TOKS, EpiToks<Cfg>, NoEpiToks> toks(args, quad, lane);
+            if constexpr (EPI_TOKS) {
+                if (args.splits == 1) toks.begin(ti, half);
+            }
             if constexpr (Cfg::EPI_ROWS) {
                 if (args.splits == 1) epi.begin(ti);
                 if (t + tile_step < num_tiles) next = decode_tile<Cfg>(args, t + tile_step, s_prefix);
@@ -1595,7 +1594,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
                 if constexpr (!Cfg::GROUPED) {
                     // cluster peers wait for this CTA on the cluster barrier: arrive anyway (the
                     // second warpgroup arrives in the teardown)
-                    if (!Cfg::RX_OWN && half == 0 && args.splits > 1 && args.cluster_size > 1) {
+                    if (!Cfg::RX_OWN && (half == 0 || Cfg::EPI != kEpiPlain) && args.splits > 1 && args.cluster_size > 1) {
                         cluster_arrive();
                         cluster_wait();
                     }
@@ -1613,8 +1612,11 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             if constexpr (Cfg::GROUPED) n_cols = min(BN, (ti.q_valid + 15) & ~15);
             if constexpr (Cfg::NARROW) n_cols = ti.q_span;
             if constexpr (!Cfg::GROUPED) {
-                if (split_k && half == 0)
+                if constexpr (Cfg::EPI != kEpiPlain && !Cfg::PAIR) {
+                    if (split_k) split.finish(ti, tacc, alpha);
+                } else if (Cfg::EPI == kEpiPlain && split_k && half == 0) {
                     split_k_epilogue<Cfg>(args, ti, smem, rx_bar, s_is_last, tacc, row, alpha, ab);
+                }
             }
             // this warpgroup's columns [c_lo, c_hi), multiples of 16
             const int mid = ((n_cols / 2 + 15) / 16) * 16;
@@ -1708,7 +1710,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
                         if (h == 1 && !two) break;
                         const int c = c0 + 16 * h;
                         if constexpr (Cfg::EPI != kEpiPlain)
-                            epi_tok16<Cfg>(args, ti, quad, lane, c, r[h], alpha);
+                            toks.run(ti, h, c, r[h], alpha);
                         else if constexpr (Cfg::SWIGLU)
                             swiglu_chunk16<Cfg>(args, ti, quad, lane, c, r[h], alpha, gsh, rcp_tab, stage_w, sstage_w);
                         else if (args.out_dtype != kOutF32)
@@ -1739,7 +1741,8 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
         // the pipeline; together with the first epilogue warpgroup's arrival (after its
         // accumulator is complete) this tells the cluster peers that this CTA's shared memory
         // may receive their partial rows
-        if ((warp < 4 || warp >= 8) && args.splits > 1 && args.cluster_size > 1) {
+        // (a fused epilogue: both warpgroups arrive after their accumulator)
+        if ((warp < 4 || (warp >= 8 && Cfg::EPI == kEpiPlain)) && args.splits > 1 && args.cluster_size > 1) {
             cluster_arrive();
             cluster_wait();
         }
