@@ -267,8 +267,8 @@ typedef enum {
  *                 + residual_scale * residual[m, n]
  * computed in fp32 and rounded once to out_dtype. sfA, sfB: NVFP4_SF_TILED. bias[N]: fp32
  * (device), or NULL for none. residual[M, N]: out_dtype elements, row-major (device), or NULL for
- * none; it may be out itself (each element is read before its place is written), but no other
- * array that overlaps out. residual_scale is a host value, not used without residual. flags:
+ * none; it may be out itself (each element is read before its place is written); any other overlap
+ * with out is NVFP4_ERR_INVALID_ARG. residual_scale is a host value, not used without residual. flags:
  * NVFP4_GEMM_B_READY as for nvfp4_gemm_ex3. No workspace: split-K reduces inside a thread-block
  * cluster, in a fixed order. Shapes and alignment as for nvfp4_gemm; bias and residual 16-byte
  * aligned. A bad act, out_dtype or flag: NVFP4_ERR_INVALID_ARG.
@@ -303,7 +303,8 @@ nvfp4_status nvfp4_gate_up_sf_tile(const uint8_t* sf, int64_t I, int64_t K, uint
  *   nvfp4_gemm_glu_backward: the gradients of g and u from dh[M, I], with g and u computed again
  *                            by the same product (the forward call stores neither):
  *                                dgu[m, j] = dh * u * act'(g),  dgu[m, I + j] = dh * act(g)
- *                            dh and dgu[M, 2 I] in dtype, dgu rounded once; they must not overlap.
+ *                            dh and dgu[M, 2 I] in dtype, dgu rounded once; an overlap of the two is
+ *                            NVFP4_ERR_INVALID_ARG.
  *                            act' is 0 at the kink of relu. The gradient of the block's input is
  *                            then nvfp4_gemm of the quantised dgu with the transposed weights.
  * I % 32 == 0 (NVFP4_SF_TILED h_sf: I % 64 == 0), otherwise shapes, alignment, flags and determinism

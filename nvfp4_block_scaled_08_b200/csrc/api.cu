@@ -109,8 +109,16 @@ nvfp4_status check_gemm_common(const void* A, const void* sfA, const void* B, co
 bool valid_out_dtype(nvfp4_out_dtype t) { return t == NVFP4_OUT_BF16 || t == NVFP4_OUT_F16 || t == NVFP4_OUT_F32; }
 bool valid_act(nvfp4_act a) { return a >= NVFP4_ACT_NONE && a <= NVFP4_ACT_RELU2; }
 
+// Whether byte ranges [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb)
+{
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 // The rest of every fused product: plan (no workspace), launch. L holds all but the error word.
-nvfp4_status launch_fused(nvfp4::GemmLaunch& L, int epilogue, cudaStream_t stream)
+// (The descriptor cache allocates host memory: nothing thrown there leaves the C boundary.)
+nvfp4_status launch_fused(nvfp4::GemmLaunch& L, int epilogue, cudaStream_t stream) try
 {
     DeviceInfo d;
     nvfp4_status st = current_device(&d);
@@ -123,6 +131,8 @@ nvfp4_status launch_fused(nvfp4::GemmLaunch& L, int epilogue, cudaStream_t strea
     const cudaError_t e = nvfp4::launch_gemm_fused(plan, L, epilogue, stream, &enc_failed);
     if (enc_failed) return NVFP4_ERR_CUDA;
     return from_cuda(e);
+} catch (...) {
+    return NVFP4_ERR_CUDA;
 }
 
 // Checks of the gated products' shapes and operands; `io` is any required 16-byte aligned array.
@@ -144,6 +154,8 @@ nvfp4_status check_norm(const nvfp4::NormLaunch& a, int64_t rows, int64_t H, nvf
     if (!a.x || !a.w || !out || (!a.y && (a.post || a.gate || a.r))) return NVFP4_ERR_INVALID_ARG;
     if (H % 8 != 0 || H > nvfp4::kMaxNormH || rows > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (a.ld_x < H || (a.y && a.ld_y < H) || (a.r && a.ld_r < H)) return NVFP4_ERR_INVALID_ARG;
+    // the residual over x or y: row by row
+    if (a.r && ((a.r == a.x && a.ld_r != a.ld_x) || (a.r == a.y && a.ld_r != a.ld_y))) return NVFP4_ERR_INVALID_ARG;
     const int64_t per16 = dtype == NVFP4_OUT_F32 ? 4 : 8;      // elements in 16 bytes
     if (!aligned16(a.x) || !aligned16(a.y) || !aligned16(a.r) || !aligned16(a.w) || !aligned16(a.b) ||
         !aligned16(a.post) || !aligned16(a.gate) || !aligned16(out) || a.ld_x % per16 != 0 ||
@@ -402,6 +414,8 @@ nvfp4_status nvfp4_gemm_epilogue(const uint8_t* A, const uint8_t* sfA, const uin
     const nvfp4_status st = check_gemm_common(A, sfA, B, sfB, alpha, out, N, K);
     if (st != NVFP4_OK) return st;
     if (!aligned16(bias) || !aligned16(residual)) return NVFP4_ERR_MISALIGNED;
+    const uint64_t bytes = static_cast<uint64_t>(M) * N * (out_dtype == NVFP4_OUT_F32 ? 4 : 2);
+    if (residual && residual != out && overlap(residual, bytes, out, bytes)) return NVFP4_ERR_INVALID_ARG;
     nvfp4::GemmLaunch L{A, sfA, B, sfB, alpha, out, M, N, K, nullptr, 0, 0, nullptr, nullptr, true,
                         static_cast<int32_t>(out_dtype)};
     L.b_ready = (flags & NVFP4_GEMM_B_READY) != 0;
@@ -473,6 +487,8 @@ nvfp4_status nvfp4_gemm_glu_backward(const uint8_t* A, const uint8_t* sfA, const
     const nvfp4_status st = check_glu(A, sfA, B, sfB, alpha, dgu, M, I, K);
     if (st != NVFP4_OK) return st;
     if (!aligned16(dh)) return NVFP4_ERR_MISALIGNED;
+    const uint64_t bytes = static_cast<uint64_t>(M) * I * (dtype == NVFP4_OUT_F32 ? 4 : 2);
+    if (overlap(dh, bytes, dgu, 2 * bytes)) return NVFP4_ERR_INVALID_ARG;
     nvfp4::GemmLaunch L{A, sfA, B, sfB, alpha, dgu, M, 2 * I, K, nullptr, 0, 0, nullptr, nullptr, true,
                         static_cast<int32_t>(dtype)};
     L.b_ready = (flags & NVFP4_GEMM_B_READY) != 0;

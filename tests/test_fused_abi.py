@@ -23,9 +23,10 @@ COMMON = [(dict(A=None), 1), (dict(sfB=None), 1), (dict(alpha=None), 1), (dict(M
 
 @pytest.mark.parametrize("bad,status", COMMON + [
     (dict(out=None), 1), (dict(N=-8), 1), (dict(dtype=3), 1), (dict(N=12), 2), (dict(N=1 << 31), 2), (dict(out=0x6008), 3),
-    (dict(bias=0x7004), 3), (dict(residual=0x8008), 3), (dict(N=0), 0)], ids=str)
+    (dict(bias=0x7004), 3), (dict(residual=0x80000008), 3), (dict(residual=0x6010), 1), (dict(residual=0x5FF0), 1), (dict(N=0), 0)],
+    ids=str)
 def test_epilogue(lib, bad, status):
-    args = dict(PTRS, out=0x6000, M=16, N=768, K=512, bias=0x7000, act=2, residual=0x8000, scale=1.0, dtype=0, flags=0, s=None)
+    args = dict(PTRS, out=0x6000, M=16, N=768, K=512, bias=0x7000, act=2, residual=0x80000000, scale=1.0, dtype=0, flags=0, s=None)
     assert call(lib.nvfp4_gemm_epilogue, args, **bad) == status
 
 
@@ -47,9 +48,10 @@ def test_glu_quantize(lib, bad, status):
 
 
 @pytest.mark.parametrize("bad,status", GLU + [
-    (dict(dh=None), 1), (dict(dgu=None), 1), (dict(dtype=-1), 1), (dict(dh=0x6004), 3), (dict(dgu=0x7004), 3)], ids=str)
+    (dict(dh=None), 1), (dict(dgu=None), 1), (dict(dtype=-1), 1), (dict(dh=0x6004), 3), (dict(dgu=0x70000004), 3),
+    (dict(dgu=0x6000), 1), (dict(dgu=0x6000 + 16 * 768 * 2 - 16), 1), (dict(dgu=0x1000), 1)], ids=str)
 def test_glu_backward(lib, bad, status):
-    args = dict(PTRS, dh=0x6000, dgu=0x7000, M=16, I=768, K=512, act=4, dtype=0, flags=0, s=None)
+    args = dict(PTRS, dh=0x6000, dgu=0x70000000, M=16, I=768, K=512, act=4, dtype=0, flags=0, s=None)
     assert call(lib.nvfp4_gemm_glu_backward, args, **bad) == status
 
 
@@ -67,7 +69,7 @@ NORM = [(dict(x=None), 1), (dict(w=None), 1), (dict(dtype=3), 1), (dict(norm=2),
         (dict(y=None, post=None, gate=None), 1), (dict(ld_x=504), 1), (dict(ld_y=0), 1), (dict(ld_r=504), 1),
         (dict(H=516, ld_x=520, ld_y=520, ld_r=520), 2), (dict(H=32832, ld_x=40000, ld_y=40000, ld_r=40000), 2), (dict(rows=1 << 31), 2),
         (dict(x=0x1004), 3), (dict(y=0x2008), 3), (dict(w=0x3004), 3), (dict(b=0x4004), 3), (dict(post=0x5004), 3), (dict(gate=0x6004), 3),
-        (dict(r=0x7004), 3), (dict(ld_x=516), 3), (dict(ld_y=516), 3), (dict(ld_r=516), 3), (dict(rows=0), 0), (dict(H=0), 0)]
+        (dict(r=0x7004), 3), (dict(r=0x1000, ld_r=520), 1), (dict(r=0x2000, ld_r=1024), 1), (dict(ld_x=516), 3), (dict(ld_y=516), 3), (dict(ld_r=516), 3), (dict(rows=0), 0), (dict(H=0), 0)]
 HEAD = dict(x=0x1000, y=0x2000, dtype=0, rows=4, H=512, ld_x=512, ld_y=512, norm=0, w=0x3000, b=0x4000, post=0x5000, gate=0x6000,
             scale=1.0, eps=1e-6, r=0x7000, ld_r=512)
 

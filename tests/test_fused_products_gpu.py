@@ -285,6 +285,55 @@ def test_gate_up_sf_tile(cuda_device):
         np.testing.assert_array_equal(got.cpu().numpy(), tile_np(interleaved(sf), K))
 
 
+@pytest.mark.parametrize("scale", [1e6, 1e22, 1e30])
+def test_large_arguments(cuda_device, scale):
+    """Activations far outside their curved range: act(z) is 0 or z (its square for relu2, where finite), act' 0
+    or 1, at any magnitude. fp32 outputs, no overflow: the up half is scaled down by its block scales."""
+    d = cuda_device
+    for M in (6, 140):
+        p = Product(d, M, 256, 256, 61, gated=True)
+        a, sa, b, sb, al = p.args
+        big = al * scale
+        v = torch.from_numpy(p.v).to(d) * scale
+        for name in ("gelu", "gelu_tanh", "silu", "relu", "none"):
+            z = v.abs() > 1e4
+            assert z.float().mean() > 0.9
+            want = v if name == "none" else v.clamp(min=0)
+            got = nv.gemm_epilogue(a, sa, b, nv.sf_tile(dev_of(p.sb, d)), big, act=name, out_dtype=torch.float32).double()
+            assert ((got - want).abs() <= 1e-5 * want.abs() + 1e-12)[z].all(), name
+            if scale < 1e15:                         # g * u stays finite
+                g, u, zz = v[:, :128], v[:, 128:], z[:, :128]
+                h = nv.gemm_glu(a, sa, b, sb, big, act=name, out_dtype=torch.float32).double()
+                want = (g if name == "none" else g.clamp(min=0)) * u
+                assert ((h - want).abs() <= 2e-5 * want.abs() + 1e-5)[zz].all(), name
+            dh = torch.ones(M, 128, device=d)
+            grad = nv.gemm_glu_backward(a, sa, b, sb, big, dh, act=name).double()
+            g, u, zz = v[:, :128], v[:, 128:], z[:, :128]
+            step = torch.ones_like(g) if name == "none" else (g > 0).double()
+            assert ((grad[:, :128] - u * step).abs() <= 1e-5 * u.abs())[zz].all(), name
+            assert ((grad[:, 128:] - g * step).abs() <= 1e-5 * (g * step).abs() + 1e-12)[zz].all(), name
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """Outputs of more than 2^31 elements: the last rows equal those of a product of the last rows alone."""
+    d, M, N, K = cuda_device, 140_000, 16_384, 256
+    assert M * N > 2 ** 31
+    rng = np.random.default_rng(5)
+    Aq, sa = operand(rng, M, K)
+    Bq, sb = operand(rng, N, K)
+    b, sbt, al = dev_of(Bq, d), dev_of(tile_np(sb, K), d), torch.tensor([ALPHA], device=d)
+    out = torch.zeros(M, N, dtype=torch.bfloat16, device=d)
+    out[-300:] = 1.5
+    nv.gemm_epilogue(dev_of(Aq, d), dev_of(tile_np(sa, K), d), b, sbt, al, out=out, residual=out, residual_scale=2.0)
+    last = (dev_of(Aq[-300:], d), dev_of(tile_np(sa[-300:], K), d), b, sbt, al)
+    want = nv.gemm_epilogue(*last, residual=torch.full((300, N), 1.5, dtype=torch.bfloat16, device=d), residual_scale=2.0)
+    assert torch.equal(out[-300:], want)
+    dh = out[:, :N // 2].contiguous()
+    del out
+    dgu = nv.gemm_glu_backward(dev_of(Aq, d), dev_of(tile_np(sa, K), d), b, sbt, al, dh)
+    assert torch.equal(dgu[-300:], nv.gemm_glu_backward(*last, dh[-300:].contiguous()))
+
+
 def test_deterministic_and_replayed(cuda_device):
     """The same bits twice, from another stream, and from a captured graph replayed on new inputs."""
     d = cuda_device

@@ -190,6 +190,27 @@ def test_large_mean_and_constant_rows(cuda_device):
     assert ((q[0] & 0x77) == 0).all() and (sf[0] == 0).all()
 
 
+def test_offsets_past_32_bits(cuda_device):
+    d, T, H = cuda_device, 270_000, 8192
+    assert T * H > 2 ** 31
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=d)
+    y = torch.zeros(T, H, dtype=torch.bfloat16, device=d)
+    c = Case(d, 50, H, torch.bfloat16, "rms", post=True, gate=True)
+    x[-50:], y[-50:] = c.x, c.y
+    out, r = nv.residual_norm(x, c.w, y, r_out=x, out=y.new_zeros(T, H), **c.kw)
+    # (not the bits of a call of 50 rows: the threads that share a row, and with them the order of its
+    # sums, go by the number of rows)
+    c.check_r(x[-50:])
+    want, e = c.expected(x[-50:])
+    check(out[-50:], want, stored(want, e, torch.bfloat16))
+    assert not out[:-50].any()
+    gs = 300.0
+    q, sf, _ = nv.residual_norm_quantize(x, c.w, torch.ones(1, device=d) * gs, eps=EPS)
+    ri, ci = torch.arange(T - 50, T)[:, None], torch.arange(H // 16)[None, :]
+    at = ((ri // 128) * (H // 64) + ci // 4) * 512 + (ri % 32) * 16 + ((ri // 32) % 4) * 4 + ci % 4
+    check_quantised(q[-50:].cpu().numpy(), sf[at.to(d)].cpu().numpy(), want, e, gs, "large")
+
+
 def test_bad_rows_stay_in_their_rows(cuda_device):
     d = cuda_device
     c = Case(d, 200, 512, torch.bfloat16, "rms", post=True)
