@@ -151,6 +151,11 @@ def _stream(stream=None) -> int:
     return stream.cuda_stream
 
 
+def _stream_of(dev: int, stream=None) -> int:
+    """_stream for the current device, whose index is known."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -294,9 +299,10 @@ OUT_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 def _out_code(out: torch.Tensor) -> int:
-    if out.dtype not in OUT_DTYPES:
+    code = OUT_DTYPES.get(out.dtype)
+    if code is None:
         raise ValueError("out must be bfloat16, float16 or float32")
-    return OUT_DTYPES[out.dtype]
+    return code
 
 
 def gemm(Aq, sfA, Bq, sfB, alpha_t, out=None, workspace=None, stream=None, tiled=False,
@@ -412,9 +418,10 @@ NORMS = {"rms": 0, "layer": 1}
 
 
 def _code(table: dict, name: str, what: str) -> int:
-    if name not in table:
+    code = table.get(name)
+    if code is None:
         raise ValueError(f"{what} must be one of {', '.join(table)}")
-    return table[name]
+    return code
 
 
 def _arg(t, name: str, dtype, dev: int, shape=None, numel: int = 0) -> int | None:
@@ -473,11 +480,14 @@ def gemm_epilogue(Aq, sfA, Bq, sfB, alpha_t, out=None, *, bias=None, act: str = 
     ops, M, N, K, dev = _operands(Aq, sfA, Bq, sfB, alpha_t)
     if out is None:
         out = torch.empty(M, N, dtype=out_dtype, device=Aq.device)
-    _check("nvfp4_gemm_epilogue", load().nvfp4_gemm_epilogue(
+    code = _out_code(out)
+    st = load().nvfp4_gemm_epilogue(
         *ops, _arg(out, "out", out.dtype, dev, (M, N)), M, N, K,
-        _arg(bias, "bias", torch.float32, dev, (N,)), _code(ACTS, act, "act"),
-        _arg(residual, "residual", out.dtype, dev, (M, N)), residual_scale, _out_code(out),
-        1 if b_ready else 0, _stream(stream)))
+        None if bias is None else _arg(bias, "bias", torch.float32, dev, (N,)), _code(ACTS, act, "act"),
+        None if residual is None else _arg(residual, "residual", out.dtype, dev, (M, N)), residual_scale, code,
+        1 if b_ready else 0, _stream_of(dev, stream))
+    if st:
+        _check("nvfp4_gemm_epilogue", st)
     return out
 
 
@@ -492,7 +502,7 @@ def gate_up_sf_tile(sf: torch.Tensor, out: torch.Tensor | None = None, stream=No
         out = torch.empty(_tiled_bytes(rows, K), dtype=torch.uint8, device=dev)
     _check("nvfp4_gate_up_sf_tile", load().nvfp4_gate_up_sf_tile(
         _arg(sf, "sf", torch.uint8, dev), rows // 2, K,
-        _arg(out, "out", torch.uint8, dev, None, _tiled_bytes(rows, K)), _stream(stream)))
+        _arg(out, "out", torch.uint8, dev, None, _tiled_bytes(rows, K)), _stream_of(dev, stream)))
     return out
 
 
@@ -513,7 +523,7 @@ def gemm_glu(Aq, sfA, Bq, sfB, alpha_t, out=None, *, act: str = "silu", out_dtyp
         out = torch.empty(M, I, dtype=out_dtype, device=dev)
     _check("nvfp4_gemm_glu", load().nvfp4_gemm_glu(
         *ops, _arg(out, "out", out.dtype, dev, (M, I)), M, I, K, _code(ACTS, act, "act"),
-        _out_code(out), 1 if b_ready else 0, _stream(stream)))
+        _out_code(out), 1 if b_ready else 0, _stream_of(dev, stream)))
     return out
 
 
@@ -533,7 +543,7 @@ def gemm_glu_quantize(Aq, sfA, Bq, sfB, alpha_t, gs_h, h_q=None, h_sf=None, *, a
         *ops, M, I, K, _code(ACTS, act, "act"), _arg(gs_h, "gs_h", torch.float32, dev, None, 1),
         _arg(h_q, "h_q", torch.uint8, dev, (M, I // 2)),
         _arg(h_sf, "h_sf", torch.uint8, dev, None, n), SF_TILED if tiled else SF_LINEAR,
-        1 if b_ready else 0, _stream(stream)))
+        1 if b_ready else 0, _stream_of(dev, stream)))
     return h_q, h_sf
 
 
@@ -547,7 +557,7 @@ def gemm_glu_backward(Aq, sfA, Bq, sfB, alpha_t, dh, out=None, *, act: str = "si
     _check("nvfp4_gemm_glu_backward", load().nvfp4_gemm_glu_backward(
         *ops, _arg(dh, "dh", out.dtype, dev, (M, I)),
         _arg(out, "out", out.dtype, dev, (M, 2 * I)), M, I, K, _code(ACTS, act, "act"),
-        _out_code(out), 1 if b_ready else 0, _stream(stream)))
+        _out_code(out), 1 if b_ready else 0, _stream_of(dev, stream)))
     return out
 
 
@@ -594,7 +604,7 @@ def residual_norm(x, weight, y=None, *, kind: str = "rms", bias=None, post_weigh
     if out is None:
         out = torch.empty(rows, H, dtype=out_dtype or x.dtype, device=dev)
     _check("nvfp4_residual_norm", load().nvfp4_residual_norm(
-        *args, _arg(out, "out", out.dtype, dev, (rows, H)), _out_code(out), _stream(stream)))
+        *args, _arg(out, "out", out.dtype, dev, (rows, H)), _out_code(out), _stream_of(dev, stream)))
     return out, r
 
 
@@ -614,7 +624,7 @@ def residual_norm_quantize(x, weight, gs, y=None, *, kind: str = "rms", bias=Non
     _check("nvfp4_residual_norm_quantize", load().nvfp4_residual_norm_quantize(
         *args, _arg(gs, "gs", torch.float32, dev, None, 1),
         _arg(q, "q", torch.uint8, dev, (rows, H // 2)),
-        _arg(sf, "sf", torch.uint8, dev, None, n), SF_TILED if tiled else SF_LINEAR, _stream(stream)))
+        _arg(sf, "sf", torch.uint8, dev, None, n), SF_TILED if tiled else SF_LINEAR, _stream_of(dev, stream)))
     return q, sf, r
 
 

@@ -232,14 +232,13 @@ struct GemmCfg {
     // and a 16-byte scale stage
     static constexpr int SWIGLU_BYTES = SWIGLU ? 1024 + kEpilogueWarps * (128 + 16) : 0;
     // split-K receive buffer: this rank's chunk (at most ceil(16 / cs) * 8 rows) from each of
-    // cs <= 8 ranks, cs * ceil(16 / cs) * 8 <= 168 rows of [BN + 4] floats (a GLU whose weights are
-    // the MMA M operand: see RX_FLOATS). Few-token (swap)
+    // cs <= 8 ranks, cs * ceil(16 / cs) * 8 <= 168 rows of [BN + 4] floats; of a GLU with SWAP 8
+    // chunks of a 32-row (g, u) group and half of the tokens, cs * ceil(8 / cs) * 32 <= 448 rows of
+    // [BN / 2 + 4] floats. Few-token (swap)
     // launches give it a region of its own (RX_OWN), so that the cluster barrier before the
     // exchange moves into the prologue; other split-K launches reuse the drained stage ring.
     static constexpr int PSTRIDE = BN + 4;
     static constexpr bool RX_OWN = SWAP && !GROUPED;
-    // (GLU and SWAP: 8 chunks of a 32-row (g, u) group and half of the tokens, cs * ceil(8 / cs) * 32
-    // <= 448 rows of [BN / 2 + 4] floats)
     static constexpr int RX_FLOATS = GLU && SWAP ? 448 * (BN / 2 + 4) : 168 * PSTRIDE;
     static constexpr int RX_BYTES = RX_OWN ? ((RX_FLOATS * 4 + 1023) & ~1023) : 0;
     // EPI_ROWS: per epilogue warp two 2 KB boxes (side input in, results out) and the bias of a
@@ -863,6 +862,10 @@ __device__ __forceinline__ float actq_quantize_t(const GemmArgs& a, uint8_t* sme
 // swap tile; EpiSplit: the split-K epilogue.
 template <class Cfg>
 struct EpiRows;
+template <class Cfg>
+struct EpiToks;
+template <class Cfg>
+struct EpiSplit;
 struct NoEpiRows {
     __device__ NoEpiRows(const GemmArgs&, const EpiMaps<false>&, int, int, int, uint8_t*, uint64_t*, const AbortState&) {}
 };
@@ -872,10 +875,6 @@ struct NoEpiToks {
 struct NoEpiSplit {
     __device__ NoEpiSplit(const GemmArgs&, uint8_t*, uint64_t*, int, int, const AbortState&) {}
 };
-template <class Cfg>
-struct EpiToks;
-template <class Cfg>
-struct EpiSplit;
 
 // Split-K epilogue of one CTA, run by the 128 threads of the first epilogue warpgroup
 // (thread = accumulator row; named barrier 2);

@@ -1,11 +1,13 @@
 """Plain fp64 references and derived error bounds of the fused products and norms.
 
 Bounds. The kernels accumulate in fp32: acc is within (K + 1) 2^-24 sum|a b| of the exact sum in any order
-(the alpha multiply included), called e_v below. Activations are evaluated in fp32 from CUDA's expf (at most
-2 ulp), erff (2 ulp) and an approximate division (2 ulp): with the few roundings around them the evaluation is
-within 2^-19 |z| of act(z) (relu2: of 2^-22 z^2), and 2^-19 (1 + |z|) of act'(z); an error e in z moves
-act(z) by at most L e, L = 1.13 bounding |act'| of all but relu2 (there 2 |z| + e), and act'(z) by at most
-1.2 e (relu: 0 away from the kink; the tests keep z off it; relu2: 2 e). A stored value adds half a step of its
+(the alpha multiply included), called e_v below. Activations are evaluated in fp32 from an exponential within
+2^-22 of an argument rounded to 2^-23, a reciprocal within 2^-22 and, for GELU, a polynomial of erfc within
+1.5e-7: each of p = sigmoid, Phi is then within 2^-20 (the argument's error counts x^2 p (1 - p) <= 0.5 times
+2^-23, or as little for GELU), so act(z) is within 2^-19 |z| (relu2: of 2^-22 z^2) and act'(z) within
+2^-19 (1 + |z|); an error e in z moves act(z) by at most L e, L = 1.13 bounding |act'| of all but relu2
+(there 2 |z| + e), and act'(z) by at most 1.2 e (relu: 0 away from the kink, and either value within e of it;
+relu2: 2 e). A stored value adds half a step of its
 type, `half_step(dtype) * |value|` (and half the smallest subnormal)."""
 from __future__ import annotations
 
