@@ -452,19 +452,18 @@ struct EpiSplit {
     const GemmArgs& a;
     const AbortState& ab;
     uint64_t* const rx_bar;
-    float* const rx;
+    const uint32_t rx;                               // the receive buffer (shared-memory address)
     const int row, half, tid, cs;
     // this row's (GROUPS: and token half's) place in its owner's receive buffer: a shared::cluster
     // address and the owner's barrier, or here (dst 0)
-    float* mine[GROUPS ? 2 : 1];
-    uint32_t dst[GROUPS ? 2 : 1], bar[GROUPS ? 2 : 1];
+    uint32_t mine[GROUPS ? 2 : 1], dst[GROUPS ? 2 : 1], bar[GROUPS ? 2 : 1];
     int k0, n, items;                                // this rank's chunks [k0, k0 + n) and their items
     Item item0;
     float side0[SV];
 
     __device__ __forceinline__ EpiSplit(const GemmArgs& args, uint8_t* smem, uint64_t* rxb, int r, int h,
                                         const AbortState& abort)
-        : a(args), ab(abort), rx_bar(rxb), rx(reinterpret_cast<float*>(smem + (Cfg::RX_OWN ? Cfg::OFF_RX : Cfg::OFF_P))),
+        : a(args), ab(abort), rx_bar(rxb), rx(smem_u32(smem + (Cfg::RX_OWN ? Cfg::OFF_RX : Cfg::OFF_P))),
           row(r), half(h), tid(128 * h + r), cs(args.cluster_size)
     {
     }
@@ -482,8 +481,8 @@ struct EpiSplit {
             const int chunk = GROUPS ? 2 * (row >> 5) + p : row >> 3;
             const int owner = chunk * cs / CHUNKS;
             const int o0 = first(owner), on = first(owner + 1) - o0;
-            mine[p] = rx + ((rank * on + chunk - o0) * CR + (row & (CR - 1))) * PS;
-            dst[p] = owner == rank ? 0u : mapa_shared(smem_u32(mine[p]), static_cast<uint32_t>(owner));
+            mine[p] = rx + 4 * ((rank * on + chunk - o0) * CR + (row & (CR - 1))) * PS;
+            dst[p] = owner == rank ? 0u : mapa_shared(mine[p], static_cast<uint32_t>(owner));
             bar[p] = owner == rank ? 0u : mapa_shared(smem_u32(rx_bar), static_cast<uint32_t>(owner));
         }
         if constexpr (SIDE) item0 = item_of(ti, tid);
@@ -560,7 +559,7 @@ struct EpiSplit {
                     const float4 f = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
                                                  __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
                     const uint32_t d = GROUPS && p ? dst[GROUPS ? 1 : 0] : dst[0];
-                    if (d == 0u) *reinterpret_cast<float4*>((GROUPS && p ? mine[GROUPS ? 1 : 0] : mine[0]) + cc) = f;
+                    if (d == 0u) sts_f4((GROUPS && p ? mine[GROUPS ? 1 : 0] : mine[0]) + 4 * cc, f);
                     else st_async_f4(d + 4 * cc, f.x, f.y, f.z, f.w, GROUPS && p ? bar[GROUPS ? 1 : 0] : bar[0]);
                 }
             }
@@ -596,14 +595,14 @@ struct EpiSplit {
 #pragma unroll
                 for (int t = 0; t < 8; ++t) v[t] = 0.0f;
                 for (int q = 0; q < cs; ++q) {
-                    const float* p = rx + q * step + it.src;
+                    const uint32_t p = rx + 4 * (q * step + it.src);
                     if constexpr (Cfg::SWAP) {
 #pragma unroll
-                        for (int t = 0; t < 8; ++t) v[t] += p[t * PS];
+                        for (int t = 0; t < 8; ++t) v[t] += lds_f32(p + 4 * t * PS);
                     } else {
 #pragma unroll
                         for (int t = 0; t < 8; t += 4) {
-                            const float4 x = *reinterpret_cast<const float4*>(p + t);
+                            const float4 x = lds_f4(p + 4 * t);
                             v[t] += x.x; v[t + 1] += x.y; v[t + 2] += x.z; v[t + 3] += x.w;
                         }
                     }
@@ -617,11 +616,11 @@ struct EpiSplit {
             } else if constexpr (GROUPS) {
                 float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};      // (two: the activations take pairs)
                 for (int q = 0; q < cs; ++q) {
-                    const float* p = rx + q * step + it.src;
+                    const uint32_t p = rx + 4 * (q * step + it.src);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        g[t] += p[t * (CW / 2)];
-                        u[t] += p[16 * PS + t * (CW / 2)];
+                        g[t] += lds_f32(p + 4 * t * (CW / 2));
+                        u[t] += lds_f32(p + 4 * (16 * PS + t * (CW / 2)));
                     }
                 }
                 int m[2];
@@ -644,9 +643,8 @@ struct EpiSplit {
             } else {
                 float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 for (int q = 0; q < cs; ++q) {
-                    const float* p = rx + q * step + it.src;
-                    const float4 x = *reinterpret_cast<const float4*>(p);
-                    const float4 y = *reinterpret_cast<const float4*>(p + 16);
+                    const uint32_t p = rx + 4 * (q * step + it.src);
+                    const float4 x = lds_f4(p), y = lds_f4(p + 64);
                     g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
                     u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
                 }
@@ -833,9 +831,9 @@ struct EpiRows {
     }
 
     // The 16-byte piece e of this lane's row in buffer b.
-    __device__ __forceinline__ uint4* slot(int b, int e) const
+    __device__ __forceinline__ uint32_t slot(int b, int e) const
     {
-        return reinterpret_cast<uint4*>(buf + b * BOX + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4));
+        return smem_u32(buf) + b * BOX + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4);
     }
 
     // Buffer b, written by every lane, to output column n. (A box past the columns still makes a
@@ -868,11 +866,11 @@ struct EpiRows {
         for (int e = 0; e < NV / PER; ++e) {
             const float* x = v + e * PER;
             if constexpr (DT == kOutF32)
-                *slot(b, e0 + e) = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                                              __float_as_uint(x[3]));
+                sts_u4(slot(b, e0 + e), make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                                   __float_as_uint(x[3])));
             else
-                *slot(b, e0 + e) = make_uint4(pack_out16x2(x[0], x[1], DT), pack_out16x2(x[2], x[3], DT),
-                                              pack_out16x2(x[4], x[5], DT), pack_out16x2(x[6], x[7], DT));
+                sts_u4(slot(b, e0 + e), make_uint4(pack_out16x2(x[0], x[1], DT), pack_out16x2(x[2], x[3], DT),
+                                                   pack_out16x2(x[4], x[5], DT), pack_out16x2(x[6], x[7], DT)));
         }
     }
     template <int32_t DT, int NV>
@@ -881,7 +879,7 @@ struct EpiRows {
         constexpr int PER = DT == kOutF32 ? 4 : 8;
 #pragma unroll
         for (int e = 0; e < NV / PER; ++e) {
-            const uint4 q = *slot(b, e0 + e);
+            const uint4 q = lds_u4(slot(b, e0 + e));
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
