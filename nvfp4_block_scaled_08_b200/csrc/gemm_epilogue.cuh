@@ -292,29 +292,52 @@ __device__ __forceinline__ void linear_act(const float* bias, int32_t act, float
 
 // ------------------------------------------------------------------ few tokens (weights as the MMA M operand)
 
-// One value of h (index j of token m), alone or with its block: the 16 lanes of a half-warp hold
-// the 16 indices of one block of the same token. `ok`: the token exists. All lanes take part.
-template <class Cfg>
-__device__ __forceinline__ void glu_put(const GemmArgs& a, int m, int j, float h, bool ok)
+// Eight tokens' values h[] of index j, quantised: the 16 lanes of a half-warp hold the 16 indices of
+// one block of each token. A reduce-scatter leaves lane i the maximum of token i % 8, so that each
+// scale is worked out once (its inverse goes back to the other lanes), and a transpose of 8 x 8
+// codes among 8 lanes leaves lane i eight neighbouring codes of token i % 8: 8 + 8 + 3 exchanges
+// and one pair of divisions for 128 values. m, ok: this lane's token i % 8 and whether it exists.
+__device__ __forceinline__ void quantise_tokens8(const GemmArgs& a, int j, const float (&h)[8], int m, bool ok)
 {
-    if constexpr (Cfg::EPI == kEpiGlu) {
-        if (ok) store_out1(a, static_cast<size_t>(m) * a.inter + j, h);
-    } else if constexpr (Cfg::EPI == kEpiGluQuant) {
-        float amax = fabsf(h), rcp;
+    const int lane = threadIdx.x & 31;
+    const float gs = __ldg(a.gs_h);
+    float v[8];
 #pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const uint32_t sf = block_scale(amax, __ldg(a.gs_h), rcp);
-        // eight lanes' codes as one word
-        uint32_t w = (f32x2_to_e2m1x2(__fmul_rn(h, rcp), 0.0f) & 0xFu) << (4 * (j & 7));
+    for (int t = 0; t < 8; ++t) v[t] = fabsf(h[t]);
 #pragma unroll
-        for (int o = 4; o >= 1; o >>= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
-        if (ok && (j & 7) == 0)
-            *reinterpret_cast<uint32_t*>(a.h_q + static_cast<int64_t>(m) * (a.inter >> 1) + (j >> 1)) = w;
-        if (ok && (j & 15) == 0) *h_sf_at(a, m, j >> 4) = static_cast<uint8_t>(sf);
+    for (int w = 4; w >= 1; w >>= 1) {
+        const bool hi = (lane & w) != 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (t >= w) break;
+            const float recv = __shfl_xor_sync(0xffffffffu, hi ? v[t] : v[t + w], w);
+            v[t] = fmaxf(hi ? v[t + w] : v[t], recv);
+        }
+    }
+    float rcp;
+    const uint32_t sf = block_scale(fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 8)), gs, rcp);
+    uint32_t w = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        const float r = __shfl_sync(0xffffffffu, rcp, (lane & 24) | t);
+        w |= (f32x2_to_e2m1x2(__fmul_rn(h[t], r), 0.0f) & 0xFu) << (4 * t);
+    }
+    constexpr uint32_t kMask[3] = {0x0000FFFFu, 0x00FF00FFu, 0x0F0F0F0Fu};
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+        const int d = 4 >> s, sh = 16 >> s;
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, w, d);
+        w = (lane & d) ? (w & ~kMask[s]) | (r >> sh & kMask[s]) : (w & kMask[s]) | (r & kMask[s]) << sh;
+    }
+    if (ok) {
+        // index of this lane's 8 codes: the lower or upper half of the block
+        const int j8 = (j & ~15) + (lane & 8);
+        *reinterpret_cast<uint32_t*>(a.h_q + static_cast<int64_t>(m) * (a.inter >> 1) + (j8 >> 1)) = w;
+        if ((lane & 8) == 0) *h_sf_at(a, m, j >> 4) = static_cast<uint8_t>(sf);
     }
 }
 
-// (g, u) pairs of h index j of the N tokens m[], with their dh (kEpiGluGrad).
+// (g, u) pairs of h index j of the N tokens m[] that exist (ok[]), with their dh (kEpiGluGrad).
 template <class Cfg, int N>
 __device__ __forceinline__ void glu_lane(const GemmArgs& a, const int (&m)[N], int j, float (&g)[N], const float (&u)[N],
                                          const bool (&ok)[N], const float (&dh)[N])
@@ -332,7 +355,16 @@ __device__ __forceinline__ void glu_lane(const GemmArgs& a, const int (&m)[N], i
     } else {
         act_apply(g, a.act_fn);
 #pragma unroll
-        for (int t = 0; t < N; ++t) glu_put<Cfg>(a, m[t], j, g[t] * u[t], ok[t]);
+        for (int t = 0; t < N; ++t) g[t] *= u[t];
+        if constexpr (Cfg::EPI == kEpiGluQuant) {
+            static_assert(N == 8, "eight consecutive tokens");
+            const int t = threadIdx.x & 7;
+            quantise_tokens8(a, j, g, m[0] + t, ok[0] && m[0] + t < a.M);
+        } else {
+#pragma unroll
+            for (int t = 0; t < N; ++t)
+                if (ok[t]) store_out1(a, static_cast<size_t>(m[t]) * a.inter + j, g[t]);
+        }
     }
 }
 
@@ -444,7 +476,10 @@ struct EpiSplit {
     static constexpr int CW = GROUPS ? BN / 2 : BN;  // columns of a chunk
     static constexpr int CHUNKS = GROUPS ? 8 : 16;
     static constexpr int PS = CW + 4;
-    static constexpr int NT = GROUPS && BN >= 32 ? 2 : 1;        // tokens of a grouped item: c and c + CW / 2
+    static constexpr bool QUANT = Cfg::EPI == kEpiGluQuant;
+    // tokens of a grouped item: c and c + CW / 2, or eight neighbours
+    static constexpr int NT = !GROUPS ? 1 : QUANT ? 8 : BN >= 32 ? 2 : 1;
+    static constexpr int TS = QUANT ? 1 : CW / 2;
     static constexpr bool SIDE = LINEAR || Cfg::EPI == kEpiGluGrad;
     static constexpr int SV = LINEAR ? 8 : GROUPS ? NT : 4;      // side elements of an item
     struct Item { int m, j, src; bool ok; };         // token (row of the output), first column, offset of source 0
@@ -496,7 +531,8 @@ struct EpiSplit {
         Item it;
         if constexpr (GROUPS) {
             // (index of the group, token, chunk): a half-warp holds one block of one token
-            const int i = item & 15, c = (item >> 4) % (CW / NT), k = (item >> 4) / (CW / NT);
+            const int i = item & 15, k = (item >> 4) / (CW / NT);
+            const int c = (item >> 4) % (CW / NT) * (QUANT ? NT : 1);
             const int chunk = k0 + k;
             it.m = ti.q0 + (chunk & 1) * CW + c;
             it.j = (ti.p0 >> 1) + 16 * (chunk >> 1) + i;
@@ -532,8 +568,8 @@ struct EpiSplit {
         if constexpr (GROUPS) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-                s[t] = it.j < a.inter && it.m + t * (CW / 2) < a.M
-                           ? side_value(a, load_side_bits(a, (it.m + t * (CW / 2)) * ld + it.j)) : 0.0f;
+                s[t] = it.j < a.inter && it.m + t * TS < a.M
+                           ? side_value(a, load_side_bits(a, (it.m + t * TS) * ld + it.j)) : 0.0f;
         } else {
             if (it.ok) load_side(a, it.m * ld + it.j, s);
         }
@@ -575,11 +611,13 @@ struct EpiSplit {
         ok = named_bar_and(2, 256, ok);
         if (!ok) return;
 
-        // 3. sum over the ranks in order and finish. Item counts are multiples of 32 wherever lanes
-        // exchange values: whole warps stay in the loop.
+        // 3. sum over the ranks in order and finish. Where lanes exchange values whole warps stay in
+        // the loop (items beyond the last repeat it and write nothing).
         const int step = n * CR * PS;                    // from one rank's copy to the next
-        for (int item = tid; item < items; item += 256) {
-            const Item it = SIDE && item == tid ? item0 : item_of(ti, item);
+        const int rounded = QUANT ? (items + 31) & ~31 : items;
+        for (int item = tid; item < rounded; item += 256) {
+            Item it = SIDE && item == tid ? item0 : item_of(ti, QUANT ? min(item, items - 1) : item);
+            if (QUANT && item >= items) it.ok = false;
             float s[SV];
             if constexpr (SIDE) {
                 if (item == tid) {
@@ -614,32 +652,29 @@ struct EpiSplit {
                 }
                 store_out8(a, static_cast<size_t>(it.m) * a.N + it.j, v);
             } else if constexpr (GROUPS) {
-                float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};      // (two: the activations take pairs)
+                constexpr int NA = NT == 1 ? 2 : NT;                 // (the activations take pairs)
+                float g[NA], u[NA], dh[NA];
+                int m[NA];
+                bool here[NA];
+#pragma unroll
+                for (int t = 0; t < NA; ++t) g[t] = u[t] = 0.0f;
                 for (int q = 0; q < cs; ++q) {
                     const uint32_t p = rx + 4 * (q * step + it.src);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        g[t] += lds_f32(p + 4 * t * (CW / 2));
-                        u[t] += lds_f32(p + 4 * (16 * PS + t * (CW / 2)));
+                        g[t] += lds_f32(p + 4 * t * TS);
+                        u[t] += lds_f32(p + 4 * (16 * PS + t * TS));
                     }
                 }
-                int m[2];
-                bool here[2];
-                float dh[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < NA; ++t) {
                     g[t] *= alpha;
                     u[t] *= alpha;
-                    m[t] = it.m + t * (CW / 2);
-                    here[t] = t < NT && m[t] < a.M && it.j < a.inter;
-                    if (SIDE && t < NT) dh[t] = s[t < SV ? t : 0];
+                    m[t] = it.m + t * TS;
+                    here[t] = t < NT && m[t] < a.M && it.j < a.inter && (!QUANT || item < items);
+                    dh[t] = SIDE && t < NT ? s[t < SV ? t : 0] : 0.0f;
                 }
-                if constexpr (NT == 2 || Cfg::EPI == kEpiGluGrad) {
-                    glu_lane<Cfg>(a, m, it.j, g, u, here, dh);
-                } else {
-                    act_apply(g, a.act_fn);
-                    glu_put<Cfg>(a, m[0], it.j, g[0] * u[0], here[0]);
-                }
+                glu_lane<Cfg>(a, m, it.j, g, u, here, dh);
             } else {
                 float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 for (int q = 0; q < cs; ++q) {
