@@ -268,10 +268,11 @@ typedef enum {
  * computed in fp32 and rounded once to out_dtype. sfA, sfB: NVFP4_SF_TILED. bias[N]: fp32
  * (device), or NULL for none. residual[M, N]: out_dtype elements, row-major (device), or NULL for
  * none; it may be out itself (each element is read before its place is written); any other overlap
- * with out is NVFP4_ERR_INVALID_ARG. residual_scale is a host value, not used without residual. flags:
- * NVFP4_GEMM_B_READY as for nvfp4_gemm_ex3. No workspace: split-K reduces inside a thread-block
- * cluster, in a fixed order. Shapes and alignment as for nvfp4_gemm; bias and residual 16-byte
- * aligned. A bad act, out_dtype or flag: NVFP4_ERR_INVALID_ARG.
+ * with out is NVFP4_ERR_INVALID_ARG. Outputs overlap no other operand, here and below.
+ * residual_scale is a host value, not used without residual. flags: NVFP4_GEMM_B_READY as for
+ * nvfp4_gemm_ex3. No workspace: split-K reduces inside a thread-block cluster, in a fixed order.
+ * Shapes and alignment as for nvfp4_gemm; bias and residual 16-byte aligned. A bad act, out_dtype
+ * or flag: NVFP4_ERR_INVALID_ARG.
  */
 nvfp4_status nvfp4_gemm_epilogue(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
                                  const float* alpha, void* out, int64_t M, int64_t N, int64_t K,
@@ -284,7 +285,7 @@ nvfp4_status nvfp4_gemm_epilogue(const uint8_t* A, const uint8_t* sfA, const uin
  * NVFP4_SF_TILED) bytes; padding rows become 0): the tiled layout of the rows taken in groups of
  * 16 gate rows and the 16 up rows of the same index, i.e. row 32 t + i of that order is gate row
  * 16 t + i, row 32 t + 16 + i up row I + 16 t + i (i < 16). I % 16 == 0, K % 64 == 0. For weights,
- * once. The codes stay as they are.
+ * once; sf and out must not overlap (NVFP4_ERR_INVALID_ARG). The codes stay as they are.
  */
 nvfp4_status nvfp4_gate_up_sf_tile(const uint8_t* sf, int64_t I, int64_t K, uint8_t* out, cudaStream_t stream);
 
@@ -344,8 +345,9 @@ typedef enum {
  *                                 layout) bytes, padding left as it is): the A operand of the
  *                                 products that read the block's input.
  * x, y, r_out: dtype elements, rows ld_x, ld_y, ld_r elements apart (each >= H, a multiple of 16
- * bytes). r_out may be NULL (r is not stored), x or y themselves (with the same row stride), but
- * overlap nothing else; out, q and sf overlap no input. weight, bias, post_weight, gate: fp32 [H].
+ * bytes). r_out may be NULL (r is not stored), x or y themselves (with the same row stride). Any
+ * other overlap of r_out, out or q with x, y or r_out is NVFP4_ERR_INVALID_ARG (so are rows of r_out
+ * between those of an x or y of another row stride); sf overlaps none of them. weight, bias, post_weight, gate: fp32 [H].
  * H % 8 == 0 (quantised: H % 16, NVFP4_SF_TILED: H % 64), H <= 32768; every pointer 16-byte aligned
  * (gs: 4). residual_scale and eps >= 0 are host values. rows == 0 or H == 0 is a no-op. One launch;
  * sums are fp32 in a fixed order (deterministic).

@@ -447,6 +447,15 @@ def _current_device(t: torch.Tensor, name: str) -> int:
     return dev
 
 
+def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
+    """An output tensor. With a stream given it belongs to that stream: memory that the current one
+    still uses is not handed out for it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _tiled_bytes(rows: int, K: int) -> int:
     return (rows + 127) // 128 * 128 * (K // 16)
 
@@ -479,7 +488,7 @@ def gemm_epilogue(Aq, sfA, Bq, sfB, alpha_t, out=None, *, bias=None, act: str = 
     dtype, which may be out itself; b_ready as for gemm."""
     ops, M, N, K, dev = _operands(Aq, sfA, Bq, sfB, alpha_t)
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype, device=Aq.device)
+        out = _empty((M, N), out_dtype, dev, stream)
     code = _out_code(out)
     st = load().nvfp4_gemm_epilogue(
         *ops, _arg(out, "out", out.dtype, dev, (M, N)), M, N, K,
@@ -499,7 +508,7 @@ def gate_up_sf_tile(sf: torch.Tensor, out: torch.Tensor | None = None, stream=No
         raise ValueError("sf must be [2I, K/16]")
     rows, K = sf.shape[0], sf.shape[1] * 16
     if out is None:
-        out = torch.empty(_tiled_bytes(rows, K), dtype=torch.uint8, device=dev)
+        out = _empty(_tiled_bytes(rows, K), torch.uint8, dev, stream)
     _check("nvfp4_gate_up_sf_tile", load().nvfp4_gate_up_sf_tile(
         _arg(sf, "sf", torch.uint8, dev), rows // 2, K,
         _arg(out, "out", torch.uint8, dev, None, _tiled_bytes(rows, K)), _stream_of(dev, stream)))
@@ -520,7 +529,7 @@ def gemm_glu(Aq, sfA, Bq, sfB, alpha_t, out=None, *, act: str = "silu", out_dtyp
     Aq [M, K/2] with tiled scales; Bq [2I, K/2] gate rows then up rows, sfB from gate_up_sf_tile."""
     ops, M, I, K, dev = _glu_operands(Aq, sfA, Bq, sfB, alpha_t)
     if out is None:
-        out = torch.empty(M, I, dtype=out_dtype, device=dev)
+        out = _empty((M, I), out_dtype, dev, stream)
     _check("nvfp4_gemm_glu", load().nvfp4_gemm_glu(
         *ops, _arg(out, "out", out.dtype, dev, (M, I)), M, I, K, _code(ACTS, act, "act"),
         _out_code(out), 1 if b_ready else 0, _stream_of(dev, stream)))
@@ -534,10 +543,10 @@ def gemm_glu_quantize(Aq, sfA, Bq, sfB, alpha_t, gs_h, h_q=None, h_sf=None, *, a
     Returns (h_q uint8 [M, I/2], h_sf: flat tiled scales, or [M, I/16] if not tiled)."""
     ops, M, I, K, dev = _glu_operands(Aq, sfA, Bq, sfB, alpha_t)
     if h_q is None:
-        h_q = torch.empty(M, I // 2, dtype=torch.uint8, device=dev)
+        h_q = _empty((M, I // 2), torch.uint8, dev, stream)
     n = _tiled_bytes(M, I) if tiled else M * (I // 16)
     if h_sf is None:
-        h_sf = torch.empty(n, dtype=torch.uint8, device=dev)
+        h_sf = _empty(n, torch.uint8, dev, stream)
         h_sf = h_sf if tiled else h_sf.view(M, I // 16)
     _check("nvfp4_gemm_glu_quantize", load().nvfp4_gemm_glu_quantize(
         *ops, M, I, K, _code(ACTS, act, "act"), _arg(gs_h, "gs_h", torch.float32, dev, None, 1),
@@ -553,7 +562,7 @@ def gemm_glu_backward(Aq, sfA, Bq, sfB, alpha_t, dh, out=None, *, act: str = "si
     dh's dtype, with g and u computed again by the same product (one kernel)."""
     ops, M, I, K, dev = _glu_operands(Aq, sfA, Bq, sfB, alpha_t)
     if out is None:
-        out = torch.empty(M, 2 * I, dtype=dh.dtype, device=dev)
+        out = _empty((M, 2 * I), dh.dtype, dev, stream)
     _check("nvfp4_gemm_glu_backward", load().nvfp4_gemm_glu_backward(
         *ops, _arg(dh, "dh", out.dtype, dev, (M, I)),
         _arg(out, "out", out.dtype, dev, (M, 2 * I)), M, I, K, _code(ACTS, act, "act"),
@@ -574,14 +583,14 @@ def _rows(t, name: str, like):
     return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
-def _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out):
+def _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out, stream):
     """The leading arguments of both residual norms, and r (allocated where y asks for it)."""
     dev = _current_device(x, "x")
     if x.dim() != 2 or x.dtype not in OUT_DTYPES:
         raise ValueError("x must be [rows, H] in bfloat16, float16 or float32")
     rows, H = x.shape
     if y is not None and r_out is None:
-        r_out = torch.empty(rows, H, dtype=x.dtype, device=x.device)
+        r_out = _empty((rows, H), x.dtype, dev, stream)
     f32, like = torch.float32, (x.shape, x.dtype, dev)
     px, ld_x = _rows(x, "x", like)
     py, ld_y = _rows(y, "y", like)
@@ -600,9 +609,9 @@ def residual_norm(x, weight, y=None, *, kind: str = "rms", bias=None, post_weigh
 
     x, y [rows, H] (bf16, fp16 or fp32, unit column stride); weight, bias, post_weight, gate fp32
     [H]; r_out may be x or y (the residual updated in place). Returns (out, r); r is x without y."""
-    args, r, rows, H, dev = _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out)
+    args, r, rows, H, dev = _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out, stream)
     if out is None:
-        out = torch.empty(rows, H, dtype=out_dtype or x.dtype, device=dev)
+        out = _empty((rows, H), out_dtype or x.dtype, dev, stream)
     _check("nvfp4_residual_norm", load().nvfp4_residual_norm(
         *args, _arg(out, "out", out.dtype, dev, (rows, H)), _out_code(out), _stream_of(dev, stream)))
     return out, r
@@ -614,12 +623,12 @@ def residual_norm_quantize(x, weight, gs, y=None, *, kind: str = "rms", bias=Non
     """residual_norm with the normed rows quantised to NVFP4 under the fixed global scale gs (fp32
     [1], device). Returns (q uint8 [rows, H/2], sf: flat tiled scales, or [rows, H/16] if not
     tiled, r)."""
-    args, r, rows, H, dev = _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out)
+    args, r, rows, H, dev = _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out, stream)
     if q is None:
-        q = torch.empty(rows, H // 2, dtype=torch.uint8, device=dev)
+        q = _empty((rows, H // 2), torch.uint8, dev, stream)
     n = _tiled_bytes(rows, H) if tiled else rows * (H // 16)
     if sf is None:
-        sf = torch.empty(n, dtype=torch.uint8, device=dev)
+        sf = _empty(n, torch.uint8, dev, stream)
         sf = sf if tiled else sf.view(rows, H // 16)
     _check("nvfp4_residual_norm_quantize", load().nvfp4_residual_norm_quantize(
         *args, _arg(gs, "gs", torch.float32, dev, None, 1),

@@ -116,6 +116,26 @@ bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb)
     return x < y + nb && y < x + na;
 }
 
+// Whether `rows` rows of `n` bytes, `ld` bytes apart from a, share a byte with [b, b + nb).
+bool rows_overlap(const void* a, int64_t rows, uint64_t n, uint64_t ld, const void* b, uint64_t nb)
+{
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const uint64_t i = y < x + n ? 0 : (y - x - n) / ld + 1;    // the first row that ends behind b
+    return i < static_cast<uint64_t>(rows) && x + i * ld < y + nb;
+}
+
+// The same of two arrays of rows; false only if no byte is shared (interleaved rows, as the columns
+// of one tensor, are told apart where their strides are equal).
+bool rows_overlap(const void* a, uint64_t lda, const void* b, uint64_t ldb, int64_t rows, uint64_t n)
+{
+    const uint64_t up = static_cast<uint64_t>(rows - 1);
+    if (!overlap(a, up * lda + n, b, up * ldb + n)) return false;
+    if (lda != ldb) return true;
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const uint64_t d = (y >= x ? y - x : x - y) % lda;
+    return d < n || d > lda - n;
+}
+
 // The rest of every fused product: plan (no workspace), launch. L holds all but the error word.
 // (The descriptor cache allocates host memory: nothing thrown there leaves the C boundary.)
 nvfp4_status launch_fused(nvfp4::GemmLaunch& L, int epilogue, cudaStream_t stream) try
@@ -154,13 +174,22 @@ nvfp4_status check_norm(const nvfp4::NormLaunch& a, int64_t rows, int64_t H, nvf
     if (!a.x || !a.w || !out || (!a.y && (a.post || a.gate || a.r))) return NVFP4_ERR_INVALID_ARG;
     if (H % 8 != 0 || H > nvfp4::kMaxNormH || rows > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (a.ld_x < H || (a.y && a.ld_y < H) || (a.r && a.ld_r < H)) return NVFP4_ERR_INVALID_ARG;
-    // the residual over x or y: row by row
-    if (a.r && ((a.r == a.x && a.ld_r != a.ld_x) || (a.r == a.y && a.ld_r != a.ld_y))) return NVFP4_ERR_INVALID_ARG;
     const int64_t per16 = dtype == NVFP4_OUT_F32 ? 4 : 8;      // elements in 16 bytes
     if (!aligned16(a.x) || !aligned16(a.y) || !aligned16(a.r) || !aligned16(a.w) || !aligned16(a.b) ||
         !aligned16(a.post) || !aligned16(a.gate) || !aligned16(out) || a.ld_x % per16 != 0 ||
         (a.y && a.ld_y % per16 != 0) || (a.r && a.ld_r % per16 != 0))
         return NVFP4_ERR_MISALIGNED;
+    // the residual over x or y: row by row, and no other overlap of an output
+    const uint64_t esz = dtype == NVFP4_OUT_F32 ? 4 : 2, n = H * esz;
+    const uint64_t lx = a.ld_x * esz, ly = a.ld_y * esz, lr = a.ld_r * esz;
+    if (a.r && ((a.r == a.x ? lr != lx : rows_overlap(a.r, lr, a.x, lx, rows, n)) ||
+                (a.r == a.y ? lr != ly : rows_overlap(a.r, lr, a.y, ly, rows, n))))
+        return NVFP4_ERR_INVALID_ARG;
+    const uint64_t bytes = a.q ? static_cast<uint64_t>(rows) * H / 2
+                               : static_cast<uint64_t>(rows) * H * (a.out_dt == NVFP4_OUT_F32 ? 4 : 2);
+    if (rows_overlap(a.x, rows, n, lx, out, bytes) || (a.y && rows_overlap(a.y, rows, n, ly, out, bytes)) ||
+        (a.r && rows_overlap(a.r, rows, n, lr, out, bytes)))
+        return NVFP4_ERR_INVALID_ARG;
     return NVFP4_OK;
 }
 
@@ -432,6 +461,8 @@ nvfp4_status nvfp4_gate_up_sf_tile(const uint8_t* sf, int64_t I, int64_t K, uint
     if (I == 0 || K == 0) return NVFP4_OK;
     if (!sf || !out) return NVFP4_ERR_INVALID_ARG;
     if (I % 16 != 0 || K % 64 != 0 || K > kMaxDim || I > kMaxDim / 2) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    const uint64_t rows = 2 * static_cast<uint64_t>(I), k16 = static_cast<uint64_t>(K) / 16;
+    if (overlap(sf, rows * k16, out, (rows + 127) / 128 * 128 * k16)) return NVFP4_ERR_INVALID_ARG;
     DeviceInfo d;
     nvfp4_status st = current_device(&d);
     if (st != NVFP4_OK) return st;

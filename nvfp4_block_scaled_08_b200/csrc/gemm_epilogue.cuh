@@ -19,8 +19,8 @@ enum : int32_t { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kAc
 // The special function unit takes 8 cycles per warp and operation where the others take one, so
 // the activations below spend it on one exponential per element and one reciprocal per two:
 // 1 / d0 = d1 (1 / (d0 d1)). Arrays come in pairs (N even; a pair's NaN or infinity stays in its
-// own element). 8192 x 6144 x 2048 on 256 x 256 tiles: 53 us without, 59 / 64 / 64 with SiLU / GELU /
-// GELU_TANH; with expf, a division per element and erff 82 / 105 / 95.
+// own element). 8192 x 6144 x 2048 on 256 x 256 tiles: 52 us without, 57 with SiLU, 64 with bias and GELU;
+// with expf, a division per element and erff 82 and 105.
 
 __device__ __forceinline__ float exp2_approx(float x)          // 2^-22 relative, subnormal results 0
 {
@@ -731,7 +731,7 @@ struct EpiSplit {
 //
 // The loops over chunks and pieces are not unrolled: the epilogue's straight-line code would
 // otherwise pass the instruction cache once per tile and warp (8192 x 6144 x 2048 without activation:
-// 68 us unrolled, with transposes among the lanes in place of the boxes; 54 so).
+// 68 us unrolled, with transposes among the lanes in place of the boxes; 52 so).
 //
 // Per 32-column piece: kEpiLinear one box of a 16-bit type or two of fp32; the gated ones 16
 // indices of h ([16 gate, 16 up] columns): half a box of a 16-bit type or one of fp32.

@@ -126,3 +126,29 @@ def test_gradient_through_frozen_weights(cuda_device, T):
     dx = nv.gemm(q, sf, gq_t, nv.sf_tile(gsf_t), al, tiled=True)
     v, e = exact_product(q, sf, gq_t, gsf_t, al)
     check(dx, v, stored(v, e, torch.bfloat16), "dx")
+
+
+def test_outputs_belong_to_the_given_stream(cuda_device):
+    """A call on another stream takes no memory that the current stream has just freed (and may still use)."""
+    b = Block(cuda_device, 40, 512, 512, "silu")
+    nq, nsf, r, hq, hsf, _ = b.forward()
+    dh = torch.ones(b.T, b.I, device=cuda_device).bfloat16()
+    s = torch.cuda.Stream()
+    calls = [
+        lambda **kw: nv.residual_norm(b.x, b.w, b.y, **kw),
+        lambda **kw: nv.residual_norm_quantize(b.x, b.w, b.gn, b.y, tiled=False, **kw),
+        lambda **kw: (nv.gate_up_sf_tile(b.gsf, **kw),),
+        lambda **kw: (nv.gemm_glu(nq, nsf, b.gq, b.gsf_t, b.al, **kw),),
+        lambda **kw: nv.gemm_glu_quantize(nq, nsf, b.gq, b.gsf_t, b.al, b.gh, tiled=False, **kw),
+        lambda **kw: (nv.gemm_glu_backward(nq, nsf, b.gq, b.gsf_t, b.al, dh, **kw),),
+        lambda **kw: (nv.gemm_epilogue(hq, hsf, b.dq, b.dsf_t, b.al_d, residual=r, **kw),),
+    ]
+    for call in calls:
+        out = call()
+        want, ptrs = [o.clone() for o in out], {o.data_ptr() for o in out}
+        torch.cuda.synchronize()
+        del out
+        out = call(stream=s)
+        s.synchronize()
+        assert not ptrs & {o.data_ptr() for o in out}
+        assert all(torch.equal(o, w) for o, w in zip(out, want))

@@ -62,6 +62,9 @@ def test_gate_up_sf_tile(lib):
     assert f(None, 16, 64, 0x2000, None) == 1
     assert f(0x1000, 24, 64, 0x2000, None) == 2
     assert f(0x1000, 16, 48, 0x2000, None) == 2
+    # 32 rows of 4 scales in, 128 out
+    for sf, out in ((0x1000, 0x1000), (0x1000, 0x1070), (0x1000, 0x0E10)):
+        assert f(sf, 16, 64, out, None) == 1
 
 
 NORM = [(dict(x=None), 1), (dict(w=None), 1), (dict(dtype=3), 1), (dict(norm=2), 1), (dict(rows=-1), 1), (dict(H=-8), 1),
@@ -84,6 +87,33 @@ def test_residual_norm(lib, bad, status):
     (dict(q=0x9008), 3), (dict(sf=0xA004), 3), (dict(gs=0x8002), 3)], ids=str)
 def test_residual_norm_quantize(lib, bad, status):
     assert call(lib.nvfp4_residual_norm_quantize, dict(HEAD, gs=0x8000, q=0x9000, sf=0xA000, layout=1, s=None), **bad) == status
+
+
+# x, y, r: 4 rows of 1024 bytes; out: 4 rows of 1024 (bf16) or 2048 bytes (fp32)
+@pytest.mark.parametrize("bad", [
+    dict(r=0x1010), dict(r=0x0FF0), dict(r=0x2400), dict(r=0x1C00), dict(out=0x1000), dict(out=0x1FF0), dict(out=0x7010),
+    dict(out=0x6010), dict(odt=2, out=0x6010), dict(out=0x2FF0),
+    # every second row of one tensor: r on the other rows but for 16 bytes, and beside an x of another stride
+    dict(x=0x10000, ld_x=1024, r=0x103F0, ld_r=1024), dict(x=0x10000, ld_x=1024, r=0x10410, ld_r=1024),
+    dict(x=0x10000, ld_x=1024, r=0x10400, ld_r=2048), dict(r=0x10000, ld_r=1024, out=0x11810)], ids=str)
+def test_residual_norm_refuses_overlap(lib, bad):
+    assert call(lib.nvfp4_residual_norm, dict(HEAD, out=0x9000, odt=0, s=None), **bad) == 1
+
+
+# the same without a shared byte: the call goes on to the device check (no GPU here: not a status of the arguments)
+@pytest.mark.parametrize("ok", [
+    dict(), dict(r=0x1000), dict(r=0x2000), dict(r=0x0), dict(x=0x10000, ld_x=1024, r=0x10400, ld_r=1024), dict(out=0x6000 - 0x800),
+    dict(r=0x10000, ld_r=4096, out=0x10400), dict(x=0x10000, ld_x=1024, y=0x10400, ld_y=1024, r=0x10400, ld_r=1024), dict(out=0x8000)], ids=str)
+def test_residual_norm_takes_neighbours(lib, ok):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("addresses of no memory: for hosts without a GPU")
+    assert call(lib.nvfp4_residual_norm, dict(HEAD, out=0x9000, odt=0, s=None), **ok) not in (0, 1, 2, 3)
+
+
+@pytest.mark.parametrize("q", [0x1000, 0x13F0, 0x0FF0 - 0x3E0, 0x2010, 0x7BF0])
+def test_residual_norm_quantize_refuses_overlap(lib, q):
+    assert call(lib.nvfp4_residual_norm_quantize, dict(HEAD, gs=0x8000, q=q, sf=0xA000, layout=1, s=None)) == 1
 
 
 def test_binding_refuses_cpu_tensors():
