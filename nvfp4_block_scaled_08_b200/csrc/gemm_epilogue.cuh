@@ -723,15 +723,19 @@ struct EpiSplit {
 // ------------------------------------------------------------------ token-major tiles
 
 // A warp's part of a token-major tile: 32 token rows (lane = row) x up to two chunks of 64
-// accumulator columns, taken in pieces of 32. Results leave, and the residual or dh comes in, as
-// boxes of 64 bytes x 32 rows by TMA through two buffers per warp (64-byte swizzle: a lane's four
-// 16-byte pieces of its row are conflict-free, and no lane exchanges data with another). The
-// boxes are requested before the accumulator is awaited where a buffer is free, and a result
-// takes the place of the side value it used.
+// accumulator columns, taken in pieces of 32. No lane exchanges data with another: results go from
+// registers to memory, 32 or 64 bytes of a row per lane in whole sectors; the residual or dh comes
+// in as boxes of 64 bytes x 32 rows by TMA into two buffers per warp (64-byte swizzle: a lane's
+// four 16-byte pieces of its row are conflict-free), the first two requested before the accumulator
+// is awaited, each next one as soon as its buffer has been read. 8192 x 6144 x 2048 without and with a
+// residual, and in fp32: 51.3, 64.5 and 105 us. (Results as boxes by TMA through the same buffers,
+// where a load waits for the store before it: 52.6, 66 and 111; the next tile's first boxes
+// requested a tile ahead: no faster.) The residual's own cost there is one of power: 90 thousand cycles
+// at 1.54 GHz against 87 at 1.75.
 //
 // The loops over chunks and pieces are not unrolled: the epilogue's straight-line code would
-// otherwise pass the instruction cache once per tile and warp (8192 x 6144 x 2048 without activation:
-// 68 us unrolled, with transposes among the lanes in place of the boxes; 52 so).
+// otherwise pass the instruction cache once per tile and warp (without activation 68 us unrolled,
+// with transposes among the lanes for the stores).
 //
 // Per 32-column piece: kEpiLinear one box of a 16-bit type or two of fp32; the gated ones 16
 // indices of h ([16 gate, 16 up] columns): half a box of a 16-bit type or one of fp32.
@@ -740,10 +744,11 @@ struct EpiRows {
     static constexpr bool LINEAR = Cfg::EPI == kEpiLinear;
     static constexpr bool GRAD = Cfg::EPI == kEpiGluGrad;
     static constexpr bool QUANT = Cfg::EPI == kEpiGluQuant;
+    static constexpr bool SIDE_IN = Cfg::EPI_SIDE;
     static constexpr int BOX = Cfg::EPI_BOX;
 
     const GemmArgs& a;
-    const EpiMaps<true>& maps;
+    const EpiMaps<SIDE_IN>& maps;
     const AbortState& ab;
     uint8_t* const buf;          // two boxes
     float* const bias_s;         // 64 floats
@@ -751,16 +756,10 @@ struct EpiRows {
     const int quad, lane, half;
     uint32_t phases = 0;         // bit b: parity of the next wait for buffer b
     uint32_t pending = 0;        // bit b: a side box is on its way into buffer b
-    int turn = 0;                // kEpiGlu: the buffer of the next box (a tile can have an odd number)
     float2 bias[2];              // of chunk 0 and 1, two columns per lane
-    // kEpiGluGrad: a second chunk's 16-bit dh box waits in registers until its buffer is free, four
-    // 16-byte pieces per lane as they come from memory (piece lane % 4 of rows lane / 4 + 8 t).
-    // (8192 x 2048 x 6144: 87 against 89 us with a load once the buffer is free. For kEpiLinear,
-    // whose two late boxes take twice the registers, the load is faster: 69 against 72 us.)
-    uint4 late[GRAD ? 4 : 1];
 
     // smem: the boxes of all epilogue warps (512-byte aligned, as their swizzle is), then their biases
-    __device__ __forceinline__ EpiRows(const GemmArgs& args, const EpiMaps<true>& m, int q, int l, int h, uint8_t* smem,
+    __device__ __forceinline__ EpiRows(const GemmArgs& args, const EpiMaps<SIDE_IN>& m, int q, int l, int h, uint8_t* smem,
                                        uint64_t* bars, const AbortState& abort)
         : a(args), maps(m), ab(abort), buf(smem + (4 * h + q) * Cfg::EPI_WARP),
           bias_s(reinterpret_cast<float*>(smem + kEpilogueWarps * Cfg::EPI_WARP + (4 * h + q) * Cfg::EPI_BIAS)),
@@ -814,34 +813,12 @@ struct EpiRows {
 
     __device__ __forceinline__ bool active(const Tile& ti) const { return ti.p0 + 32 * quad < a.M; }
 
-    // What the tile reads first: the boxes that fit the buffers, and the late ones.
+    // The tile's first two boxes.
     template <bool F32>
     __device__ __forceinline__ void request_first(const Tile& ti)
     {
-        if (lane == 0) bulk_wait_read<0>();
         request<F32>(ti, 0, 0);
-        if (LINEAR) request<F32>(ti, 1, 1);          // (GRAD's second buffer takes du)
-        if (GRAD && !F32 && chunks(ti) == 2) {
-            const int n = first_col<false>(ti, 1) + 8 * (lane & 3);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int64_t m = ti.p0 + 32 * quad + (lane >> 2) + 8 * t;
-                late[t] = make_uint4(0u, 0u, 0u, 0u);
-                if (m < a.M && n < a.inter)
-                    late[t] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.side) + m * a.inter + n);
-            }
-        }
-    }
-
-    // The late box into buffer 0 (free).
-    __device__ __forceinline__ void late_box()
-    {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int r = (lane >> 2) + 8 * t;
-            *reinterpret_cast<uint4*>(buf + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)) = late[t];
-        }
-        __syncwarp();
+        if (LINEAR || F32 || chunks(ti) == 2) request<F32>(ti, 1, 1);
     }
 
     __device__ __forceinline__ void begin(const Tile& ti)
@@ -871,43 +848,7 @@ struct EpiRows {
         return smem_u32(buf) + b * BOX + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4);
     }
 
-    // Buffer b, written by every lane, to output column n. (A box past the columns still makes a
-    // bulk group, so that buffers_free<1> means "the other buffer" everywhere.)
-    template <bool F32>
-    __device__ __forceinline__ void send(const Tile& ti, int b, int n)
-    {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (n < end_col()) tma_store_2d(&maps.out, buf + b * BOX, n * (F32 ? 4 : 2), ti.p0 + 32 * quad);
-            bulk_commit();
-        }
-    }
-
-    // Lane 0 waits until all but the latest N stores have left their buffers.
-    template <int N>
-    __device__ __forceinline__ void buffers_free()
-    {
-        if (lane == 0) bulk_wait_read<N>();
-        __syncwarp();
-    }
-
-    // NV values as output elements of type DT in pieces e0 .. of buffer b, and back.
-    template <int32_t DT, int NV>
-    __device__ __forceinline__ void put(int b, int e0, const float* v) const
-    {
-        constexpr int PER = DT == kOutF32 ? 4 : 8;   // elements per 16-byte piece
-#pragma unroll
-        for (int e = 0; e < NV / PER; ++e) {
-            const float* x = v + e * PER;
-            if constexpr (DT == kOutF32)
-                sts_u4(slot(b, e0 + e), make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                                                   __float_as_uint(x[3])));
-            else
-                sts_u4(slot(b, e0 + e), make_uint4(pack_out16x2(x[0], x[1], DT), pack_out16x2(x[2], x[3], DT),
-                                                   pack_out16x2(x[4], x[5], DT), pack_out16x2(x[6], x[7], DT)));
-        }
-    }
+    // NV side values of type DT from pieces e0 .. of buffer b.
     template <int32_t DT, int NV>
     __device__ __forceinline__ void get(int b, int e0, float* v) const
     {
@@ -929,6 +870,36 @@ struct EpiRows {
         }
     }
 
+    // NV values to columns n .. of this lane's output row (`ld` columns, of which those below `end`
+    // are to be written), in 32-byte sectors where the address allows.
+    template <int32_t DT, int NV>
+    __device__ __forceinline__ void store_row(const Tile& ti, int ld, int n, int end, const float* v) const
+    {
+        constexpr int PER = DT == kOutF32 ? 4 : 8, ESZ = 16 / PER;   // elements per 16-byte piece, bytes of one
+        const int m = ti.p0 + 32 * quad + lane;
+        if (m >= a.M) return;
+        uint4 w[NV / PER];
+#pragma unroll
+        for (int e = 0; e < NV / PER; ++e) {
+            const float* x = v + e * PER;
+            if constexpr (DT == kOutF32)
+                w[e] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+            else
+                w[e] = make_uint4(pack_out16x2(x[0], x[1], DT), pack_out16x2(x[2], x[3], DT), pack_out16x2(x[4], x[5], DT),
+                                  pack_out16x2(x[6], x[7], DT));
+        }
+        uint8_t* p = static_cast<uint8_t*>(a.out) + (static_cast<size_t>(m) * ld + n) * ESZ;
+        if (((reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(ld) * ESZ) & 31) == 0) {
+#pragma unroll
+            for (int e = 0; e < NV / PER; e += 2)
+                if (n + e * PER < end) st_global_32(p + 16 * e, w[e], w[e + 1]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < NV / PER; ++e)
+                if (n + e * PER < end) *reinterpret_cast<uint4*>(p + 16 * e) = w[e];
+        }
+    }
+
     // Piece h (32 columns, r) of chunk k: one box of a 16-bit type, two of fp32.
     template <int32_t DT, bool SIDE>
     __device__ __forceinline__ bool linear_piece(const Tile& ti, int k, int h, const uint32_t (&r)[32], float alpha)
@@ -943,24 +914,19 @@ struct EpiRows {
         for (int s = 0; s < BOXES; ++s) {
             const int u = BOXES * (2 * k + h) + s, b = u & 1;
             if constexpr (SIDE) {
-                if (u >= 1 && u + 1 < 2 * BOXES * chunks(ti)) {   // the other buffer is the next box's
-                    buffers_free<0>();
-                    request<F32>(ti, u + 1, b ^ 1);
-                }
                 if (!landed(b)) return false;
                 float x[NV];
                 get<DT, NV>(b, 0, x);
+                __syncwarp();
+                if (u + 2 < 2 * BOXES * chunks(ti)) request<F32>(ti, u + 2, b);
                 const f32x2 sc = pack2(a.side_scale, a.side_scale);
 #pragma unroll
                 for (int i = 0; i < NV; i += 2) {
                     float* w = v + NV * s + i;
                     unpack2(fma2(sc, pack2(x[i], x[i + 1]), pack2(w[0], w[1])), w[0], w[1]);
                 }
-            } else {
-                buffers_free<1>();
             }
-            put<DT, NV>(b, 0, v + NV * s);
-            send<F32>(ti, b, first_col<F32>(ti, u));
+            store_row<DT, NV>(ti, a.N, first_col<F32>(ti, u), a.N, v + NV * s);
         }
         return true;
     }
@@ -979,34 +945,26 @@ struct EpiRows {
             unpack2(mul2(al, pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]))), g[i], g[i + 1]);
             unpack2(mul2(al, pack2(__uint_as_float(r[16 + i]), __uint_as_float(r[17 + i]))), w[i], w[i + 1]);
         }
+        const int j = ((ti.q0 + chunk_col(ti, k)) >> 1) + 16 * h;    // first index of h
         if constexpr (GRAD) {
-            if ((F32 || h == 0) && u > 0) {
-                buffers_free<0>();
-                if constexpr (F32) request<F32>(ti, u, 0);
-                else late_box();
-            }
+            const int b = u & 1;
             float d[16], x[16];
+            if (!landed(b)) return false;
+            get<DT, 16>(b, e0, x);
+            if (F32 || h == 1) {
+                __syncwarp();
+                if (u + 2 < (F32 ? 2 : 1) * chunks(ti)) request<F32>(ti, u + 2, b);
+            }
             act_apply_grad(g, d, a.act_fn);
-            if (!landed(0)) return false;
-            get<DT, 16>(0, e0, x);
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
                 const f32x2 s = pack2(x[i], x[i + 1]);
                 unpack2(mul2(mul2(pack2(d[i], d[i + 1]), pack2(w[i], w[i + 1])), s), d[i], d[i + 1]);
                 unpack2(mul2(pack2(g[i], g[i + 1]), s), g[i], g[i + 1]);
             }
-            put<DT, 16>(0, e0, d);
-            put<DT, 16>(1, e0, g);
-            if (F32 || h == 1) {
-                const int n = first_col<F32>(ti, u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && n < a.inter) {
-                    constexpr int esz = F32 ? 4 : 2;
-                    tma_store_2d(&maps.out, buf, n * esz, ti.p0 + 32 * quad);
-                    tma_store_2d(&maps.out, buf + BOX, (a.inter + n) * esz, ti.p0 + 32 * quad);
-                    bulk_commit();
-                }
+            if (j < a.inter) {
+                store_row<DT, 16>(ti, a.N, j, a.N, d);
+                store_row<DT, 16>(ti, a.N, a.inter + j, a.N, g);
             }
             return true;
         }
@@ -1015,7 +973,6 @@ struct EpiRows {
         for (int i = 0; i < 16; i += 2) unpack2(mul2(pack2(g[i], g[i + 1]), pack2(w[i], w[i + 1])), g[i], g[i + 1]);
         if constexpr (QUANT) {
             // one NVFP4 block per piece; a row's two blocks of a chunk leave together
-            const int j0 = ((ti.q0 + chunk_col(ti, k)) >> 1) + 16 * h;
             float amax = 0.0f, rcp, lo[8], hi[8];
 #pragma unroll
             for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(g[i]));
@@ -1030,19 +987,14 @@ struct EpiRows {
                 sf = s;
             } else {
                 const int m = ti.p0 + 32 * quad + lane;
-                if (m < a.M && j0 < a.inter) {
-                    *reinterpret_cast<uint4*>(a.h_q + static_cast<int64_t>(m) * (a.inter >> 1) + ((j0 - 16) >> 1)) =
+                if (m < a.M && j < a.inter) {
+                    *reinterpret_cast<uint4*>(a.h_q + static_cast<int64_t>(m) * (a.inter >> 1) + ((j - 16) >> 1)) =
                         make_uint4(q[0], q[1], q[2], q[3]);
-                    *reinterpret_cast<uint16_t*>(h_sf_at(a, m, (j0 >> 4) - 1)) = static_cast<uint16_t>(sf | s << 8);
+                    *reinterpret_cast<uint16_t*>(h_sf_at(a, m, (j >> 4) - 1)) = static_cast<uint16_t>(sf | s << 8);
                 }
             }
         } else {
-            if (F32 || h == 0) buffers_free<1>();
-            put<DT, 16>(turn, e0, g);
-            if (F32 || h == 1) {
-                send<F32>(ti, turn, first_col<F32>(ti, u));
-                turn ^= 1;
-            }
+            store_row<DT, 16>(ti, a.inter, j, a.inter, g);
         }
         return true;
     }
@@ -1108,13 +1060,11 @@ struct EpiRows {
         return finish_type<kOutBF16>(ti, tacc, alpha, drained);
     }
 
-    // Before the CTA's shared memory is released: every box has landed and every store has read.
+    // Before the CTA's shared memory is released: every box has landed.
     __device__ __forceinline__ void drain()
     {
         for (int b = 0; b < 2; ++b)
             if (pending >> b & 1u) mbar_wait_drain(&bar[b], phases >> b & 1u);
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
     }
 };
 

@@ -110,14 +110,14 @@ struct GemmArgs {
     int32_t h_sf_tiled;       // kEpiGluQuant: h_sf in the tiled layout (1) or row-major (0)
 };
 
-// Tensor maps of a fused epilogue's output and side input (residual, dh): rows of elements, boxes
-// of 64 bytes x 32 rows. An empty parameter elsewhere.
+// Tensor map of a fused epilogue's side input (residual, dh): rows of elements, boxes of 64 bytes x
+// 32 rows. An empty parameter elsewhere.
 template <bool ON>
 struct EpiMaps {
 };
 template <>
 struct EpiMaps<true> {
-    CUtensorMap out, side;
+    CUtensorMap side;
 };
 
 template <int BN_, bool SWAP_, bool GROUPED_, bool SFT_ = false, bool SWIGLU_ = false, bool MX_ = false,
@@ -182,6 +182,7 @@ struct GemmCfg {
                   "fused epilogues serve the dense NVFP4 product with tiled scales: few-token tiles, "
                   "128-wide tiles and CTA pairs");
     static constexpr bool EPI_ROWS = EPI != kEpiPlain && !SWAP;   // token-major fused tiles
+    static constexpr bool EPI_SIDE = EPI_ROWS && (EPI == kEpiLinear || EPI == kEpiGluGrad);   // that read residual or dh
     static constexpr int ACTQ_BYTES = ACTQ ? 1024 + 64 + 64 : 0;   // gs / e4m3 table, maxima slots, reduction
     static_assert(!SFT || BN % 128 == 0 || (SWAP && BN <= 64), "Q tiles on 128-row tile boundaries");
     static_assert(!GROUPED || SWAP, "grouped GEMM runs with weights as the MMA M operand");
@@ -241,13 +242,13 @@ struct GemmCfg {
     static constexpr bool RX_OWN = SWAP && !GROUPED;
     static constexpr int RX_FLOATS = GLU && SWAP ? 448 * (BN / 2 + 4) : 168 * PSTRIDE;
     static constexpr int RX_BYTES = RX_OWN ? ((RX_FLOATS * 4 + 1023) & ~1023) : 0;
-    // EPI_ROWS: per epilogue warp two 2 KB boxes (side input in, results out) and the bias of a
-    // 64-column chunk. Costs 128-wide tiles one of their six ring stages; CTA pairs keep all five
+    // EPI_SIDE: per epilogue warp two 2 KB boxes of the side input and the bias of a 64-column
+    // chunk. Costs 128-wide tiles one of their six ring stages; CTA pairs keep all five
     // (a fourth KB per warp would cost them one: 5-11% of 8192 x 6144 x 2048 and larger).
     static constexpr int EPI_BOX = 2048;
     static constexpr int EPI_WARP = 2 * EPI_BOX;
     static constexpr int EPI_BIAS = EPI == kEpiLinear ? 256 : 0;
-    static constexpr int EPI_BYTES = EPI_ROWS ? kEpilogueWarps * (EPI_WARP + EPI_BIAS) : 0;
+    static constexpr int EPI_BYTES = EPI_SIDE ? kEpilogueWarps * (EPI_WARP + EPI_BIAS) : 0;
     static constexpr int MISC_BYTES = 1024 + (GROUPED ? 4 * (kMaxExperts + 1) : 0) + SWIGLU_BYTES + RX_BYTES +
                                       ACTQ_BYTES + EPI_BYTES;
     static constexpr int ALIGN_SLACK = 1024;
@@ -267,8 +268,8 @@ struct GemmCfg {
     // barriers: full, sfready, empty [STAGES]; acc_full, acc_empty [2]; mma_done; split-K rx;
     // sf_free [2]; activations quantised, slice maxima received (ACTQ); GPAIR: this CTA's
     // scales landed [STAGES]
-    // EPI_ROWS: side input landed, two per epilogue warp
-    static constexpr int NUM_BARS = 4 * STAGES + 10 + (EPI_ROWS ? 2 * kEpilogueWarps : 0);
+    // EPI_SIDE: side input landed, two per epilogue warp
+    static constexpr int NUM_BARS = 4 * STAGES + 10 + (EPI_SIDE ? 2 * kEpilogueWarps : 0);
     static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;     // tmem base, flags
     static constexpr int OFF_PREFIX = OFF_MISC + 64;
     static constexpr int OFF_SWIGLU = OFF_PREFIX + (GROUPED ? ((4 * (kMaxExperts + 1) + 15) & ~15) : 0);
@@ -1049,7 +1050,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_sfp, const __grid_constant__ CUtensorMap tm_sfq,
                   const __grid_constant__ CUtensorMap tm_q_half, const GemmArgs args,
-                  const __grid_constant__ EpiMaps<Cfg::EPI_ROWS> tm_epi)
+                  const __grid_constant__ EpiMaps<Cfg::EPI_SIDE> tm_epi)
 {
     constexpr int BN = Cfg::BN;
     constexpr int STAGES = Cfg::STAGES;
@@ -1071,7 +1072,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
     uint64_t* actq_bar = bars + 3 * STAGES + 8;     // ACTQ: the Q stages hold the activations
     uint64_t* amax_bar = bars + 3 * STAGES + 9;     // ACTQ: the peers' slice maxima arrived
     uint64_t* sf_full_bar = bars + 3 * STAGES + 10; // GPAIR: this CTA's scales of stage s landed
-    uint64_t* side_bar = bars + 4 * STAGES + 10;    // EPI_ROWS: side input boxes landed, two per warp
+    uint64_t* side_bar = bars + 4 * STAGES + 10;    // EPI_SIDE: side input boxes landed, two per warp
     uint32_t* s_tmem_base = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
     volatile int* s_is_last = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 8);
@@ -1096,7 +1097,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             mbar_init(&acc_empty_bar[s], Cfg::PAIR ? 2 * kEpilogueWarps : kEpilogueWarps);
             mbar_init(&sf_free_bar[s], Cfg::PAIR ? 8 : 4);   // the second epilogue warpgroup(s)
         }
-        if constexpr (Cfg::EPI_ROWS) {
+        if constexpr (Cfg::EPI_SIDE) {
             for (int s = 0; s < 2 * kEpilogueWarps; ++s) mbar_init(&side_bar[s], 1);
         }
         mbar_init(mma_done_bar, 1);
@@ -1115,8 +1116,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             prefetch_tensormap(&tm_sfq);
         }
         if constexpr (Cfg::NARROW) prefetch_tensormap(&tm_q_half);
-        if constexpr (Cfg::EPI_ROWS && Cfg::EPI != kEpiGluQuant) {
-            prefetch_tensormap(&tm_epi.out);
+        if constexpr (Cfg::EPI_SIDE) {
             if (args.side != nullptr) prefetch_tensormap(&tm_epi.side);
         }
     }
@@ -1586,8 +1586,8 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             }
             bool ok = mbar_wait(&acc_full_bar[acc], acc_phase, ab, kErrEpiAccFull);
             // (the warps of a fused token-major tile share nothing, and with bias, activation and
-            // residual each goes on by itself: 8192 x 6144 x 2048 with a residual 64.6 against 65.9
-            // us, in fp32 110 against 115. The gated products, which gain nothing, keep the barrier.)
+            // residual each goes on by itself: 8192 x 6144 x 2048 with a residual 64.6 against 65.9 us. The
+            // gated products, which gain nothing, keep the barrier.)
             if (Cfg::EPI_ROWS && Cfg::EPI == kEpiLinear && args.splits == 1) ok = __all_sync(0xffffffffu, ok);
             else ok = named_bar_and(1, 32 * kEpilogueWarps, ok);
             if (!ok) {
@@ -1731,7 +1731,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             if (++acc == Cfg::ACC_STAGES) { acc = 0; acc_phase ^= 1u; }
 
         }
-        if constexpr (Cfg::EPI_ROWS) epi.drain();
+        if constexpr (Cfg::EPI_SIDE) epi.drain();
     }
 
     // ------------------------------------------------------------------ teardown

@@ -78,7 +78,7 @@ static cudaError_t run(const GemmPlan& plan, const GemmLaunch& L, cudaStream_t s
     const uint64_t kb = static_cast<uint64_t>(L.K / 2);    // packed bytes per row
     const uint64_t ks = static_cast<uint64_t>(L.K / 16);   // scale bytes per row
     CUtensorMap tp, tq, tsp, tsq, tq_half;
-    EpiMaps<Cfg::EPI_ROWS> em;
+    EpiMaps<Cfg::EPI_SIDE> em;
     std::memset(&em, 0, sizeof(em));
     bool ok = true;
     GemmArgs a;
@@ -137,15 +137,11 @@ static cudaError_t run(const GemmPlan& plan, const GemmLaunch& L, cudaStream_t s
         // PAIR, BN = 256: each CTA's 64 rows of a 256 x 128 half tile
         if constexpr (Cfg::NARROW && GLU_Q) ok &= get_map_swiglu(&tq_half, Q, kb, I, 1, 128, true, BN / 4 / 32);
         else if constexpr (Cfg::NARROW) ok &= get_map(&tq_half, Q, 2, kb, q_rows, 1, kb, 0, 128, BN / 4, true);
-        if constexpr (Cfg::EPI_ROWS && EPI != kEpiGluQuant) {
-            // the output and the side input in boxes of 64 bytes x 32 rows
+        if constexpr (Cfg::EPI_SIDE) {
+            // the side input in boxes of 64 bytes x 32 rows
             const uint64_t esz = L.out_dtype == kOutF32 ? 4 : 2;
-            const uint64_t out_cols = EPI == kEpiGlu ? I : static_cast<uint64_t>(L.N);
-            const uint64_t side_cols = EPI == kEpiGluGrad ? I : static_cast<uint64_t>(L.N);
             const uint32_t box[2] = {64, 32};
-            const uint64_t od[2] = {out_cols * esz, static_cast<uint64_t>(L.M)};
-            const uint64_t sd[2] = {side_cols * esz, static_cast<uint64_t>(L.M)};
-            ok &= get_map_nd(&em.out, L.out, 2, od, od, box, kSwizzle64);
+            const uint64_t sd[2] = {(EPI == kEpiGluGrad ? I : static_cast<uint64_t>(L.N)) * esz, static_cast<uint64_t>(L.M)};
             if (L.side) ok &= get_map_nd(&em.side, L.side, 2, sd, sd, box, kSwizzle64);
         }
         if constexpr (EPI != kEpiPlain) {

@@ -62,9 +62,7 @@ template <> struct Vec8<float> {
     __device__ void store(float* p, bool wide) const
     {
         if (wide) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                         ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
-                         : "memory");
+            st_global_32(p, lo, hi);
         } else {
             reinterpret_cast<uint4*>(p)[0] = lo;
             reinterpret_cast<uint4*>(p)[1] = hi;
