@@ -19,7 +19,7 @@ enum : int32_t { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kAc
 // The special function unit takes 8 cycles per warp and operation where the others take one, so
 // the activations below spend it on one exponential per element and one reciprocal per two:
 // 1 / d0 = d1 (1 / (d0 d1)). Arrays come in pairs (N even; a pair's NaN or infinity stays in its
-// own element). 8192 x 6144 x 2048 on 256 x 256 tiles: 52 us without, 57 with SiLU, 64 with bias and GELU;
+// own element). 8192 x 6144 x 2048 on 256 x 256 tiles: 51 us without, 57 with SiLU, 63 with bias and GELU;
 // with expf, a division per element and erff 82 and 105.
 
 __device__ __forceinline__ float exp2_approx(float x)          // 2^-22 relative, subnormal results 0
@@ -297,10 +297,9 @@ __device__ __forceinline__ void linear_act(const float* bias, int32_t act, float
 // scale is worked out once (its inverse goes back to the other lanes), and a transpose of 8 x 8
 // codes among 8 lanes leaves lane i eight neighbouring codes of token i % 8: 8 + 8 + 3 exchanges
 // and one pair of divisions for 128 values. m, ok: this lane's token i % 8 and whether it exists.
-__device__ __forceinline__ void quantise_tokens8(const GemmArgs& a, int j, const float (&h)[8], int m, bool ok)
+__device__ __forceinline__ void quantise_tokens8(const GemmArgs& a, float gs, int j, const float (&h)[8], int m, bool ok)
 {
     const int lane = threadIdx.x & 31;
-    const float gs = __ldg(a.gs_h);
     float v[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t) v[t] = fabsf(h[t]);
@@ -337,9 +336,25 @@ __device__ __forceinline__ void quantise_tokens8(const GemmArgs& a, int j, const
     }
 }
 
+// One token's value h of index j, quantised: a half-warp holds the block. 4 + 3 exchanges.
+__device__ __forceinline__ void quantise_token(const GemmArgs& a, float gs, int j, float h, int m, bool ok)
+{
+    float amax = fabsf(h), rcp;
+#pragma unroll
+    for (int w = 8; w >= 1; w >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, w));
+    const uint32_t sf = block_scale(amax, gs, rcp);
+    uint32_t w = (f32x2_to_e2m1x2(__fmul_rn(h, rcp), 0.0f) & 0xFu) << (4 * (j & 7));
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1) w |= __shfl_xor_sync(0xffffffffu, w, d);
+    if (ok && (j & 7) == 0) {
+        *reinterpret_cast<uint32_t*>(a.h_q + static_cast<int64_t>(m) * (a.inter >> 1) + (j >> 1)) = w;
+        if ((j & 15) == 0) *h_sf_at(a, m, j >> 4) = static_cast<uint8_t>(sf);
+    }
+}
+
 // (g, u) pairs of h index j of the N tokens m[] that exist (ok[]), with their dh (kEpiGluGrad).
 template <class Cfg, int N>
-__device__ __forceinline__ void glu_lane(const GemmArgs& a, const int (&m)[N], int j, float (&g)[N], const float (&u)[N],
+__device__ __forceinline__ void glu_lane(const GemmArgs& a, float gs, const int (&m)[N], int j, float (&g)[N], const float (&u)[N],
                                          const bool (&ok)[N], const float (&dh)[N])
 {
     if constexpr (Cfg::EPI == kEpiGluGrad) {
@@ -357,9 +372,13 @@ __device__ __forceinline__ void glu_lane(const GemmArgs& a, const int (&m)[N], i
 #pragma unroll
         for (int t = 0; t < N; ++t) g[t] *= u[t];
         if constexpr (Cfg::EPI == kEpiGluQuant) {
-            static_assert(N == 8, "eight consecutive tokens");
-            const int t = threadIdx.x & 7;
-            quantise_tokens8(a, j, g, m[0] + t, ok[0] && m[0] + t < a.M);
+            if constexpr (N == 2) {                  // one token (the second is padding)
+                quantise_token(a, gs, j, g[0], m[0], ok[0]);
+            } else {
+                static_assert(N == 8, "eight consecutive tokens");
+                const int t = threadIdx.x & 7;
+                quantise_tokens8(a, gs, j, g, m[0] + t, ok[0] && m[0] + t < a.M);
+            }
         } else {
 #pragma unroll
             for (int t = 0; t < N; ++t)
@@ -382,6 +401,7 @@ struct EpiToks {
     const int quad, lane;
     uint32_t side[LINEAR ? NT : GRAD ? NT / 2 : 1];
     float bias = 0.0f;
+    float gs = 0.0f;             // kEpiGluQuant: gs_h, asked for before the accumulator is awaited
 
     __device__ __forceinline__ EpiToks(const GemmArgs& args, int q, int l) : a(args), quad(q), lane(l) {}
 
@@ -395,6 +415,7 @@ struct EpiToks {
     {
         const int c_lo = half ? (Cfg::BN == 16 ? 16 : Cfg::BN / 2) : 0;
         if (c_lo >= Cfg::BN) return;
+        if constexpr (Cfg::EPI == kEpiGluQuant) gs = __ldg(a.gs_h);
         if constexpr (LINEAR) {
             const int n = ti.p0 + 32 * quad + lane;
             if (a.bias != nullptr && n < a.N) bias = __ldg(a.bias + n);
@@ -452,7 +473,7 @@ struct EpiToks {
                 u[i] = up ? hi : other;
                 s[i] = GRAD ? side_value(a, side[GRAD ? (NT == 32 ? 8 * h : 0) + i : 0]) : 0.0f;
             }
-            glu_lane<Cfg>(a, m, j0 + (lane & 15), g, u, ok, s);
+            glu_lane<Cfg>(a, gs, m, j0 + (lane & 15), g, u, ok, s);
         }
     }
 };
@@ -466,7 +487,8 @@ struct EpiToks {
 // accumulator rows; where a gated product's weights are those rows, one group of 16 gate and 16 up
 // rows for half of the tokens, so that every pair and block of h has one owner (8 such chunks of
 // 32 rows over at most 8 ranks). begin(), before the accumulator is awaited, works out where
-// everything goes (divisions by the cluster size) and requests the first residual or dh elements.
+// everything goes (divisions by the cluster size) and requests gs_h (at its use it cost
+// 0.2 of 7 us) and the first residual or dh elements.
 template <class Cfg>
 struct EpiSplit {
     static constexpr int BN = Cfg::BN;
@@ -477,8 +499,9 @@ struct EpiSplit {
     static constexpr int CHUNKS = GROUPS ? 8 : 16;
     static constexpr int PS = CW + 4;
     static constexpr bool QUANT = Cfg::EPI == kEpiGluQuant;
-    // tokens of a grouped item: c and c + CW / 2, or eight neighbours
-    static constexpr int NT = !GROUPS ? 1 : QUANT ? 8 : BN >= 32 ? 2 : 1;
+    // tokens of a grouped item: c and c + CW / 2, or, quantised, eight neighbours; one where that
+    // already makes at most an item per thread (BN = 16)
+    static constexpr int NT = !GROUPS || BN == 16 ? 1 : QUANT ? 8 : 2;
     static constexpr int TS = QUANT ? 1 : CW / 2;
     static constexpr bool SIDE = LINEAR || Cfg::EPI == kEpiGluGrad;
     static constexpr int SV = LINEAR ? 8 : GROUPS ? NT : 4;      // side elements of an item
@@ -495,6 +518,7 @@ struct EpiSplit {
     int k0, n, items;                                // this rank's chunks [k0, k0 + n) and their items
     Item item0;
     float side0[SV];
+    float gs = 0.0f;                                 // QUANT: gs_h, asked for in begin()
 
     __device__ __forceinline__ EpiSplit(const GemmArgs& args, uint8_t* smem, uint64_t* rxb, int r, int h,
                                         const AbortState& abort)
@@ -520,6 +544,7 @@ struct EpiSplit {
             dst[p] = owner == rank ? 0u : mapa_shared(mine[p], static_cast<uint32_t>(owner));
             bar[p] = owner == rank ? 0u : mapa_shared(smem_u32(rx_bar), static_cast<uint32_t>(owner));
         }
+        if constexpr (QUANT) gs = __ldg(a.gs_h);
         if constexpr (SIDE) item0 = item_of(ti, tid);
         if constexpr (SIDE) {
             if (a.side != nullptr && tid < items) load_item_side(item0, side0);
@@ -674,7 +699,7 @@ struct EpiSplit {
                     here[t] = t < NT && m[t] < a.M && it.j < a.inter && (!QUANT || item < items);
                     dh[t] = SIDE && t < NT ? s[t < SV ? t : 0] : 0.0f;
                 }
-                glu_lane<Cfg>(a, m, it.j, g, u, here, dh);
+                glu_lane<Cfg>(a, gs, m, it.j, g, u, here, dh);
             } else {
                 float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 for (int q = 0; q < cs; ++q) {
@@ -705,7 +730,7 @@ struct EpiSplit {
                         float amax = fmaxf(fmaxf(fabsf(g[0]), fabsf(g[1])), fmaxf(fabsf(g[2]), fabsf(g[3]))), rcp;
                         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                        const uint32_t sf = block_scale(amax, __ldg(a.gs_h), rcp);
+                        const uint32_t sf = block_scale(amax, gs, rcp);
                         const uint32_t q = f32x2_to_e2m1x2(__fmul_rn(g[0], rcp), __fmul_rn(g[1], rcp)) |
                                            f32x2_to_e2m1x2(__fmul_rn(g[2], rcp), __fmul_rn(g[3], rcp)) << 8;
                         if (it.ok) {
@@ -757,6 +782,7 @@ struct EpiRows {
     uint32_t phases = 0;         // bit b: parity of the next wait for buffer b
     uint32_t pending = 0;        // bit b: a side box is on its way into buffer b
     float2 bias[2];              // of chunk 0 and 1, two columns per lane
+    float gs = 0.0f;             // QUANT: gs_h
 
     // smem: the boxes of all epilogue warps (512-byte aligned, as their swizzle is), then their biases
     __device__ __forceinline__ EpiRows(const GemmArgs& args, const EpiMaps<SIDE_IN>& m, int q, int l, int h, uint8_t* smem,
@@ -765,6 +791,7 @@ struct EpiRows {
           bias_s(reinterpret_cast<float*>(smem + kEpilogueWarps * Cfg::EPI_WARP + (4 * h + q) * Cfg::EPI_BIAS)),
           bar(bars + 2 * (4 * h + q)), quad(q), lane(l), half(h)
     {
+        if constexpr (QUANT) gs = __ldg(a.gs_h);
     }
 
     // Chunks of the tile in this warp's order: the last columns of the tile first for the second
@@ -976,7 +1003,7 @@ struct EpiRows {
             float amax = 0.0f, rcp, lo[8], hi[8];
 #pragma unroll
             for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(g[i]));
-            const uint32_t s = block_scale(amax, __ldg(a.gs_h), rcp);
+            const uint32_t s = block_scale(amax, gs, rcp);
 #pragma unroll
             for (int i = 0; i < 8; ++i) { lo[i] = g[i]; hi[i] = g[8 + i]; }
             q[2] = scale_to_e2m1x8(lo, rcp);
