@@ -415,10 +415,10 @@ struct EpiToks {
     {
         const int c_lo = half ? (Cfg::BN == 16 ? 16 : Cfg::BN / 2) : 0;
         if (c_lo >= Cfg::BN) return;
-        if constexpr (Cfg::EPI == kEpiGluQuant) gs = __ldg(a.gs_h);
+        if constexpr (Cfg::EPI == kEpiGluQuant) gs = ld_written(a.gs_h);
         if constexpr (LINEAR) {
             const int n = ti.p0 + 32 * quad + lane;
-            if (a.bias != nullptr && n < a.N) bias = __ldg(a.bias + n);
+            if (a.bias != nullptr && n < a.N) bias = ld_written(a.bias + n);
             if (a.side != nullptr) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
@@ -544,7 +544,7 @@ struct EpiSplit {
             dst[p] = owner == rank ? 0u : mapa_shared(mine[p], static_cast<uint32_t>(owner));
             bar[p] = owner == rank ? 0u : mapa_shared(smem_u32(rx_bar), static_cast<uint32_t>(owner));
         }
-        if constexpr (QUANT) gs = __ldg(a.gs_h);
+        if constexpr (QUANT) gs = ld_written(a.gs_h);
         if constexpr (SIDE) item0 = item_of(ti, tid);
         if constexpr (SIDE) {
             if (a.side != nullptr && tid < items) load_item_side(item0, side0);
@@ -791,7 +791,7 @@ struct EpiRows {
           bias_s(reinterpret_cast<float*>(smem + kEpilogueWarps * Cfg::EPI_WARP + (4 * h + q) * Cfg::EPI_BIAS)),
           bar(bars + 2 * (4 * h + q)), quad(q), lane(l), half(h)
     {
-        if constexpr (QUANT) gs = __ldg(a.gs_h);
+        if constexpr (QUANT) gs = ld_written(a.gs_h);
     }
 
     // Chunks of the tile in this warp's order: the last columns of the tile first for the second
@@ -863,7 +863,7 @@ struct EpiRows {
                 for (int k = 0; k < 2; ++k) {
                     const int n = ti.q0 + chunk_col(ti, k) + 2 * lane;
                     bias[k] = make_float2(0.0f, 0.0f);
-                    if (k < chunks(ti) && n < a.N) bias[k] = __ldg(reinterpret_cast<const float2*>(a.bias + n));
+                    if (k < chunks(ti) && n < a.N) bias[k] = ld_written(reinterpret_cast<const float2*>(a.bias + n));
                 }
             }
         }

@@ -810,7 +810,7 @@ __device__ __forceinline__ float actq_quantize_t(const GemmArgs& a, uint8_t* sme
     float amax = 0.0f;
     for (int r = 0; r < cs; ++r) amax = fmaxf(amax, slots[r]);
     const float gs = (amax == 0.0f) ? 1.0f : __fdiv_rn(2688.0f, amax);
-    const float alpha = __fdiv_rn(1.0f, __fmul_rn(gs, __ldg(a.gs_b)));
+    const float alpha = __fdiv_rn(1.0f, __fmul_rn(gs, ld_written(a.gs_b)));
     {
         const float sfd = e4m3_to_f32(static_cast<uint32_t>(e));
         rcp_tab[e] = (sfd == 0.0f) ? 0.0f : __fdiv_rn(gs, sfd);
@@ -1555,7 +1555,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
         }
         if constexpr (Cfg::SWIGLU) {
             // gs_h / e4m3(s) for all 256 scale codes, once per CTA (one entry per epilogue thread)
-            gsh = __ldg(args.gs_h);
+            gsh = ld_written(args.gs_h);
             const uint32_t code = threadIdx.x - 128;
             const float sfd = e4m3_to_f32(code);
             rcp_tab[code] = (sfd == 0.0f) ? 0.0f : __fdiv_rn(gsh, sfd);
@@ -1604,7 +1604,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             tc_fence_after();
 
             const float alpha = Cfg::ACTQ ? actq_alpha
-                              : Cfg::GROUPED ? __ldg(args.alpha + ti.expert) : __ldg(args.alpha);
+                              : Cfg::GROUPED ? ld_written(args.alpha + ti.expert) : ld_written(args.alpha);
             const uint32_t tacc = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + acc * BN;
             const int p = ti.p0 + row;             // P row this thread owns
             const bool split_k = !Cfg::GROUPED && args.splits > 1;

@@ -27,7 +27,7 @@ namespace nvfp4 {
 namespace {
 
 // 16-byte load that leaves no line in L1 (rows are read once; the weights stay there). Not the
-// read-only path: r may be written over x or y.
+// read-only path: r may be written over x or y, and the kernel before may have written both.
 __device__ __forceinline__ uint4 load16(const void* p)
 {
     uint4 v;
@@ -114,16 +114,18 @@ __device__ __forceinline__ void store_as(void* out, int64_t idx, const float (&v
     w.store(static_cast<T*>(out) + idx, wide);
 }
 
+// Eight weights. p is behind_wait(): the kernel before may have written them (a gate that it
+// worked out, say), so they are neither constant data nor free to be loaded before the wait; behind
+// it the compiler may place the loads as it likes (no output overlaps them).
 __device__ __forceinline__ void load_weights(const float* p, float (&v)[8], bool wide)
 {
     if (wide) {
-        asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
             : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
             : "l"(p));
     } else {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        asm("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p));
+        asm("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(p + 4));
     }
 }
 
@@ -206,6 +208,7 @@ __global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) residual_norm_kernel(co
     const int64_t row = TPR <= 32 ? blockIdx.x * static_cast<int64_t>(blockDim.x / TPR) + threadIdx.x / TPR : blockIdx.x;
     grid_dependency_wait();
     grid_launch_dependents();
+    const float *w_n = behind_wait(a.w), *b_n = behind_wait(a.b), *w_post = behind_wait(a.post), *w_gate = behind_wait(a.gate);
     // rows past the last one (TPR <= 32) hold nothing, but stay for their warp's exchanges
     const int nvec = row < a.rows ? a.H >> 3 : 0;
     const bool wide = a.wide != 0;
@@ -231,9 +234,9 @@ __global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) residual_norm_kernel(co
         for (int k = 0; k < V; ++k) yw[k].decode(z[k]);
         if (a.post) {
             normalise<TPR, V>(a, z, in, red, slot);
-            multiply<TPR, V>(z, in, t, a.post, wide);
+            multiply<TPR, V>(z, in, t, w_post, wide);
         }
-        if (a.gate) multiply<TPR, V>(z, in, t, a.gate, wide);
+        if (a.gate) multiply<TPR, V>(z, in, t, w_gate, wide);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             if (!in[k]) continue;
@@ -251,16 +254,16 @@ __global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) residual_norm_kernel(co
         for (int k = 0; k < V; ++k) xw[k].decode(z[k]);
     }
     normalise<TPR, V>(a, z, in, red, slot);
-    const float gs = QUANT ? __ldg(a.gs) : 0.0f;
+    const float gs = QUANT ? ld_written(a.gs) : 0.0f;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int c = t + k * TPR;
         if (in[k]) {
             float w[8];
-            load_weights(a.w + 8 * c, w, wide);
+            load_weights(w_n + 8 * c, w, wide);
             if (a.b) {
                 float b[8];
-                load_weights(a.b + 8 * c, b, wide);
+                load_weights(b_n + 8 * c, b, wide);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) z[k][i] = fmaf(z[k][i], w[i], b[i]);
             } else {

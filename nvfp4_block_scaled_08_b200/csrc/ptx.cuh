@@ -591,6 +591,31 @@ __device__ __forceinline__ void grid_dependency_wait()
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Loads of what the previous kernel may have written, for use behind grid_dependency_wait(). Not
+// __ldg and not ld.global.nc: this kernel may have started while that one still wrote, and a load
+// that is said to be of constant data need not stay behind the wait. Volatile, so that it does.
+__device__ __forceinline__ float ld_written(const float* p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_written(const float2* p)
+{
+    float2 v;
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+    return v;
+}
+
+// The same for many loads that the compiler may place among other work: p, known only from here
+// on (volatile statements keep their order), so that a load through it cannot come before.
+template <typename T>
+__device__ __forceinline__ const T* behind_wait(const T* p)
+{
+    asm volatile("" : "+l"(p));
+    return p;
+}
+
 // ... and allow the next grid in the stream, if launched with the attribute, to start.
 __device__ __forceinline__ void grid_launch_dependents()
 {

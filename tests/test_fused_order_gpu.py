@@ -1,0 +1,81 @@
+"""The fused calls directly behind the kernels that write their vectors and scalars: a gate or bias that a product
+works out, a global scale, an alpha. Those kernels let the next one start early; the results have to be those of
+calls with the device idle in between."""
+import pytest
+import torch
+
+import nvfp4_block_scaled_08_b200 as nv
+from nvfp4_block_scaled_08_b200 import workloads
+
+pytestmark = pytest.mark.gpu
+
+
+def quantised(x):
+    gs = nv.global_scale(x)
+    q, sf = nv.quantize(x, gs)
+    return q, nv.sf_tile(sf), gs, sf
+
+
+@pytest.mark.parametrize("T,H", [(1, 1024), (40, 1024), (300, 2048)])
+def test_vectors_written_just_before(cuda_device, T, H):
+    """gate, weight, bias and post_weight are rows of fp32 products launched just before the norm."""
+    d = cuda_device
+    cond = workloads.normal(4, 2048, 1.0, 11).to(d)
+    mod = workloads.normal(H, 2048, 0.02, 12).to(d)
+    a, sa, ga, _ = quantised(cond)
+    b, sb, gb, _ = quantised(mod)
+    al = nv.alpha(ga, gb)
+    x, y = workloads.normal(T, H, 1.0, 13).to(d).bfloat16(), workloads.normal(T, H, 1.0, 14).to(d).bfloat16()
+    gs = torch.full((1,), 300.0, device=d)
+
+    def run(idle, scale):
+        vec = torch.full((4, H), 1e9, device=d)      # what a load before the wait would see
+        alpha = al * scale
+        torch.cuda.synchronize()
+        nv.gemm_epilogue(a, sa, b, sb, alpha, out=vec)
+        if idle:
+            torch.cuda.synchronize()
+        kw = dict(kind="layer", bias=vec[1], post_weight=vec[2], gate=vec[3])
+        out = nv.residual_norm(x, vec[0], y, **kw)
+        nv.gemm_epilogue(a, sa, b, sb, alpha, out=vec)
+        q = nv.residual_norm_quantize(x, vec[0], gs, y, tiled=False, **kw)
+        torch.cuda.synchronize()
+        return (*out, *q, vec)
+
+    for scale in (1.0, 0.5, 2.0):
+        want = run(True, scale)
+        for _ in range(5):
+            assert all(torch.equal(g, w) for g, w in zip(run(False, scale), want))
+
+
+@pytest.mark.parametrize("M", [1, 64, 300])
+def test_scalars_and_bias_written_just_before(cuda_device, M):
+    """alpha, gs_h and the bias come from kernels launched just before the products that read them."""
+    d, H, I = cuda_device, 1024, 512
+    x = workloads.normal(M, H, 1.0, 21).to(d)
+    w = workloads.normal(2 * I, H, 0.05, 22).to(d)
+    a, sa, ga, _ = quantised(x)
+    b, sb, gb, rows = quantised(w)
+    sg = nv.gate_up_sf_tile(rows)
+    wide = workloads.normal(2000, 4096, 3.0, 23).to(d)
+    first = nv.alpha(ga, gb)
+
+    def run(idle):
+        vec = torch.full((M, 2 * I), 1e9, device=d)
+        wait = torch.cuda.synchronize if idle else (lambda: None)
+        torch.cuda.synchronize()
+        nv.gemm_epilogue(a, sa, b, sb, first, out=vec)
+        wait()
+        lin = nv.gemm_epilogue(a, sa, b, sb, first, bias=vec[M - 1], act="gelu")
+        gs_h = nv.global_scale(wide)
+        wait()
+        q, sf = nv.gemm_glu_quantize(a, sa, b, sg, first, gs_h, tiled=False)
+        al = nv.alpha(ga, gb)
+        wait()
+        h = nv.gemm_glu(a, sa, b, sg, al)
+        torch.cuda.synchronize()
+        return lin, q, sf, h
+
+    want = run(True)
+    for _ in range(5):
+        assert all(torch.equal(g, w) for g, w in zip(run(False), want))

@@ -1,0 +1,37 @@
+"""CPU checks of what the sources of the fused kernels must keep to and no run can show."""
+import os
+import re
+
+import pytest
+
+import nvfp4_block_scaled_08_b200 as nv
+
+CSRC = os.path.join(os.path.dirname(nv.__file__), "csrc")
+
+
+def code(name):
+    """The file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+@pytest.mark.parametrize("name", ["norm.cu", "gemm_kernel.cuh", "gemm_epilogue.cuh"])
+def test_no_constant_data_loads(name):
+    """These kernels may start while the kernel before them still writes, so nothing is loaded as data that is
+    constant while they run: such a load need not stay behind the wait for that kernel."""
+    text = code(name)
+    assert not re.findall(r"__ldg\b|\.nc\b|__constant__", text)
+    # global loads without volatile are ordered by their address alone: only in load_weights, of pointers
+    # that behind_wait() gave
+    loose = re.findall(r"asm\s*\(\s*\"ld\.global[^;]*;", text)
+    if name != "norm.cu":
+        assert not loose
+        return
+    body = text[text.index("void load_weights"):]
+    body = body[:body.index("\n}\n")]
+    assert len(loose) == body.count("ld.global") == 3
+    tied = set(re.findall(r"(\w+) = behind_wait\(a\.\w+\)", text))
+    assert tied == {"w_n", "b_n", "w_post", "w_gate"}
+    used = set(re.findall(r"load_weights\((\w+) \+ 8", text)) | set(re.findall(r"multiply<TPR, V>\(z, in, t, (\w+),", text))
+    assert used == tied | {"weights"}                # `weights`: multiply's own parameter
+    assert text.index("grid_dependency_wait();") < text.index("behind_wait(a.")
