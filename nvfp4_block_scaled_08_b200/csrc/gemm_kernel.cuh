@@ -1636,6 +1636,9 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
                             }
                         }
                     });
+                    // a side box has timed out: no further tile, whose boxes would go to the same
+                    // buffers and barriers; drain() waits for those still on their way
+                    if (!ok) break;
                 }
             } else if constexpr (Cfg::SF_IN_ACC) {
                 // the second warpgroup frees the last 64 columns (the next tile's scale

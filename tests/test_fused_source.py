@@ -35,3 +35,14 @@ def test_no_constant_data_loads(name):
     used = set(re.findall(r"load_weights\((\w+) \+ 8", text)) | set(re.findall(r"multiply<TPR, V>\(z, in, t, (\w+),", text))
     assert used == tied | {"weights"}                # `weights`: multiply's own parameter
     assert text.index("grid_dependency_wait();") < text.index("behind_wait(a.")
+
+
+def test_a_timed_out_side_box_ends_the_tile_loop():
+    """The epilogue's result decides about the next tile: after a time-out its boxes would be sent into buffers,
+    and armed on barriers, that one is still on its way to."""
+    text = code("gemm_kernel.cuh")
+    call = text.index("ok = epi.finish(")
+    end = text.index("});", call)
+    assert re.match(r"\}\);\s*if \(!ok\) break;", text[end:]), text[end:end + 80]
+    # and what is still pending is waited for behind the loop, before the shared memory is released
+    assert text.index("epi.drain();") > end
