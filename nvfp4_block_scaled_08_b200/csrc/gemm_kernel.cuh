@@ -1750,12 +1750,12 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             cluster_wait();
         }
     }
-    if constexpr (Cfg::RX_OWN) {
-        // split-K with a receive region of its own: no cluster barrier. Every byte a peer sends
-        // to this CTA (partial rows; ACTQ: slice maxima) is counted on this CTA's own rx (amax)
-        // barrier, which its epilogue has waited for, so nothing is still on its way here when
-        // it leaves. After an abort those waits may not have completed: wait for them once more,
-        // bounded, so that no peer's rows land in the shared memory of a CTA that has left.
+    if constexpr (!Cfg::GROUPED && !Cfg::PAIR) {
+        // split-K: no cluster barrier behind the exchange. Every byte a peer sends to this CTA
+        // (partial rows; ACTQ: slice maxima) is counted on this CTA's own rx (amax) barrier, which
+        // its epilogue has waited for, so nothing is still on its way here when it leaves. After
+        // an abort those waits may not have completed: wait for them once more, bounded, so that
+        // no peer's rows land in the shared memory of a CTA that has left.
         if (warp == 4 && lane == 0 && args.splits > 1 && args.cluster_size > 1) {
             if (!mbar_test_wait(rx_bar, 0)) mbar_wait_drain(rx_bar, 0);
             if constexpr (Cfg::ACTQ) {

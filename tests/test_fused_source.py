@@ -46,3 +46,13 @@ def test_a_timed_out_side_box_ends_the_tile_loop():
     assert re.match(r"\}\);\s*if \(!ok\) break;", text[end:]), text[end:end + 80]
     # and what is still pending is waited for behind the loop, before the shared memory is released
     assert text.index("epi.drain();") > end
+
+
+def test_every_split_k_launch_drains_its_receive_barrier():
+    """A CTA that has given up waits, bounded, for its peers' rows before its shared memory is released: with a
+    receive region of its own and with the reused stage ring."""
+    text = code("gemm_kernel.cuh")
+    at = text.index("mbar_wait_drain(rx_bar, 0)")
+    guards = re.findall(r"if constexpr \(([^;]*?)\) \{", text[:at])
+    assert guards[-1] == "!Cfg::GROUPED && !Cfg::PAIR"
+    assert text.rindex("if (warp == 4 && lane == 0 && args.splits > 1 && args.cluster_size > 1)", 0, at) > text.rindex(guards[-1], 0, at)
