@@ -250,7 +250,14 @@ nvfp4_status nvfp4_gemm_ex3(const uint8_t* A, const uint8_t* sfA, const uint8_t*
                             nvfp4_sf_layout sf_layout, nvfp4_out_dtype out_dtype, uint32_t flags,
                             cudaStream_t stream);
 
-/* Activation functions of the fused products, evaluated in fp32. */
+/*
+ * Activation functions of the fused products, evaluated in fp32 from the fp32 argument v. Beside
+ * the rounding to the output type act(v) is off by at most, relative to itself,
+ *     GELU 2^-19 + v^2 2^-23,  SILU 2^-20 + |v| 2^-23,  GELU_TANH 2^-20 + |w| 2^-21
+ * with w = 2 sqrt(2 / pi) (v + 0.044715 v^3); in the negative tails GELU is 0 where exp(-v^2 / 2) is
+ * below 2^-126, SILU and GELU_TANH may be off by 2^-54 where v or w is below -41.5. The derivatives
+ * of the three (nvfp4_gemm_glu_backward) are off by at most 2^-19 (1 + |v|).
+ */
 typedef enum {
     NVFP4_ACT_NONE = 0,
     NVFP4_ACT_RELU = 1,       /* max(v, 0) */
