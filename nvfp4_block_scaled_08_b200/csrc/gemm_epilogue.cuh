@@ -508,6 +508,7 @@ struct EpiSplit {
     // already makes at most an item per thread (BN = 16)
     static constexpr int NT = !GROUPS || BN == 16 ? 1 : QUANT ? 8 : 2;
     static constexpr int TS = QUANT ? 1 : CW / 2;
+    static_assert(!QUANT || (GROUPS ? 16 * (CW / NT) : CR * (BN / 8)) % 32 == 0, "a chunk's items fill whole warps");
     static constexpr bool SIDE = LINEAR || Cfg::EPI == kEpiGluGrad;
     static constexpr int SV = LINEAR ? 8 : GROUPS ? NT : 4;      // side elements of an item
     struct Item { int m, j, src; bool ok; };         // token (row of the output), first column, offset of source 0
@@ -641,13 +642,11 @@ struct EpiSplit {
         ok = named_bar_and(2, 256, ok);
         if (!ok) return;
 
-        // 3. sum over the ranks in order and finish. Where lanes exchange values whole warps stay in
-        // the loop (items beyond the last repeat it and write nothing).
+        // 3. sum over the ranks in order and finish. (QUANT: lanes exchange values, in whole warps of
+        // items.)
         const int step = n * CR * PS;                    // from one rank's copy to the next
-        const int rounded = QUANT ? (items + 31) & ~31 : items;
-        for (int item = tid; item < rounded; item += 256) {
-            Item it = SIDE && item == tid ? item0 : item_of(ti, QUANT ? min(item, items - 1) : item);
-            if (QUANT && item >= items) it.ok = false;
+        for (int item = tid; item < items; item += 256) {
+            const Item it = SIDE && item == tid ? item0 : item_of(ti, item);
             float s[SV];
             if constexpr (SIDE) {
                 if (item == tid) {
@@ -701,7 +700,7 @@ struct EpiSplit {
                     g[t] *= alpha;
                     u[t] *= alpha;
                     m[t] = it.m + t * TS;
-                    here[t] = t < NT && m[t] < a.M && it.j < a.inter && (!QUANT || item < items);
+                    here[t] = t < NT && m[t] < a.M && it.j < a.inter;
                     dh[t] = SIDE && t < NT ? s[t < SV ? t : 0] : 0.0f;
                 }
                 glu_lane<Cfg>(a, gs, m, it.j, g, u, here, dh);
