@@ -144,16 +144,23 @@ def _check(fn: str, status: int):
         raise Nvfp4Error(fn, status, msg)
 
 
+def _public_raw_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# The current stream's raw handle and the current device's index: torch's own bindings, which build
+# no Stream object (3 us a call), or its public functions where a torch version lacks them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream=None) -> int:
-    # the current stream's raw handle (torch.cuda.current_stream() builds a Stream object: 3 us)
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+    return _raw_stream(_device()) if stream is None else stream.cuda_stream
 
 
 def _stream_of(dev: int, stream=None) -> int:
     """_stream for the current device, whose index is known."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _ptr(t: torch.Tensor | None):
@@ -442,7 +449,7 @@ def _arg(t, name: str, dtype, dev: int, shape=None, numel: int = 0) -> int | Non
 def _current_device(t: torch.Tensor, name: str) -> int:
     """The index of the current CUDA device, which must be t's."""
     dev = t.get_device()                 # -1: not a CUDA tensor
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    if dev < 0 or dev != _device():
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     return dev
 
