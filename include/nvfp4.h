@@ -356,8 +356,11 @@ typedef enum {
  * other overlap of r_out, out or q with x, y or r_out is NVFP4_ERR_INVALID_ARG (so are rows of r_out
  * between those of an x or y of another row stride); sf overlaps none of them. weight, bias, post_weight, gate: fp32 [H].
  * H % 8 == 0 (quantised: H % 16, NVFP4_SF_TILED: H % 64), H <= 32768; every pointer 16-byte aligned
- * (gs: 4). residual_scale and eps >= 0 are host values. rows == 0 or H == 0 is a no-op. One launch;
- * sums are fp32 in a fixed order (deterministic).
+ * (gs: 4). residual_scale and eps >= 0 are host values. rows == 0 or H == 0 is a no-op. One launch.
+ * Sums are fp32 in an order that the shape and dtype fix: the same call gives the same bits, but
+ * calls with more rows than the device has SMs sum a row in another order than calls with at most
+ * as many, so that a row's last bits may differ between two batch sizes. Squares are summed in
+ * fp32: rows whose sum of squares overflows it (|z| of 2^64 / sqrt(H) and more) have no meaningful n.
  */
 nvfp4_status nvfp4_residual_norm(const void* x, const void* y, nvfp4_out_dtype dtype, int64_t rows, int64_t H,
                                  int64_t ld_x, int64_t ld_y, nvfp4_norm norm, const float* weight, const float* bias,

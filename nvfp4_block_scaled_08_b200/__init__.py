@@ -615,7 +615,8 @@ def residual_norm(x, weight, y=None, *, kind: str = "rms", bias=None, post_weigh
     own norm times post_weight (if given) and gate * v (if given); out = N(r) * weight + bias.
 
     x, y [rows, H] (bf16, fp16 or fp32, unit column stride); weight, bias, post_weight, gate fp32
-    [H]; r_out may be x or y (the residual updated in place). Returns (out, r); r is x without y."""
+    [H]; r_out may be x or y (the residual updated in place). Returns (out, r); r is x without y.
+    A row's last bits may differ between batches of more and of at most as many rows as SMs."""
     args, r, rows, H, dev = _norm_args(x, weight, y, kind, bias, post_weight, gate, residual_scale, eps, r_out, stream)
     if out is None:
         out = _empty((rows, H), out_dtype or x.dtype, dev, stream)

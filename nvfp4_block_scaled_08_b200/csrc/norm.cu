@@ -341,7 +341,8 @@ cudaError_t launch_t(const NormLaunch& a, cudaStream_t stream, int num_sms)
 {
     // Threads per row: as few as hold the row in four vectors each (16384 x 6144 bf16 with post_weight
     // and gate on 256 threads 139 us, on 512 160), two of fp32 (16384 x 8192 on 512 threads 315 us,
-    // on 256 344); with no more rows than SMs the row is spread wider, one vector per thread.
+    // on 256 344); with no more rows than SMs the row is spread wider, one vector per thread. (The
+    // threads of a row set the order of its sums: batches on the two sides may differ in last bits.)
     const int64_t v = a.rows <= num_sms ? 1 : sizeof(T) == 4 ? 2 : 4;
     if (a.H <= 64) return launch_v<T, 8>(a, stream);
     if (a.H <= 128) return launch_v<T, 16>(a, stream);
