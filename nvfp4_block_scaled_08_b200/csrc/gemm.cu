@@ -136,8 +136,13 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool allow_workspace, int nu
     // same MMA work. Measured on B200: 16384^3 in 1528-1577 us against 1771-1850 us, 8192^3 in
     // 193-194 us against 215-224 us, 4096^3 in 30.3 us against 32.7 us, 8192 x 4096 x 6144 in
     // 77.6 us against 84.5 us; with 8 K stages (4096 x 6144 x 2048) single CTAs win, 28.8
-    // against 30.8 us. 256 x 128 pair tiles (the override with bn = 128) lost to 256 x 256
-    // ones on every shape measured.
+    // against 30.8 us. 256 x 128 pair tiles (the override with bn = 128) are slower than 256 x 256
+    // ones where those fill the machine (4096^3 36.7 against 31.8 us, 8192 x 6144 x 2048 60.7
+    // against 53.9, 1024 x 4096 x 6144 17.5 against 14.6), but faster where one round leaves SMs
+    // idle (500 x 2048 x 6144 10.1 us against 12.6, and 11.7 for this plan; 256 x 2048 x 6144 10.0
+    // against 12.6 and 10.5; 100 x 6144 x 2048 6.0 against 7.5 and 8.8). This planner does not take
+    // them, nor pairs of 256 x 256 with 8 K stages where those are now the faster ones (8192 x 6144 x
+    // 2048 62 us as single CTAs, 2001 x 6144 x 2048 18.4 against 17.4): plan_fused below does both.
     // 1: off, 2: wherever possible, 3: the planner's pairs without half tiles
     const int fp = g_force_pair.load(std::memory_order_relaxed);
     const bool pair_shape = !p.swap && p.splits == 1 && p.p_tiles >= 2;

@@ -1,6 +1,8 @@
 // gemm_fused.cu -- the dense NVFP4 product with a fused epilogue: bias, activation and residual,
-// the gated feed-forward product (16- or 32-bit or NVFP4 output) and its gradients. Same
-// kernel, tiling and planner as the plain product (gemm.cu); tiled scales only.
+// the gated feed-forward product (16- or 32-bit or NVFP4 output) and its gradients. The
+// kernel of the plain product (gemm.cu) on its few-token tiles, on 128 x 128 tiles and on CTA pairs
+// (256 x 128, 256 x 256; no single-CTA tiles wider than 128), with a planner of its own (plan_fused);
+// tiled scales only.
 #include "gemm_epilogue.cuh"
 #include "gemm_launch.cuh"
 
