@@ -19,7 +19,7 @@ enum : int32_t { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kAc
 // The special function unit takes 8 cycles per warp and operation where the others take one, so
 // the activations below spend it on one exponential per element and one reciprocal per two:
 // 1 / d0 = d1 (1 / (d0 d1)). Arrays come in pairs (N even; a pair's NaN or infinity stays in its
-// own element). 8192 x 6144 x 2048 on 256 x 256 tiles: 51 us without, 57 with SiLU, 63 with bias and GELU;
+// own element). 8192 x 6144 x 2048 on 256 x 256 tiles: 51.5 us without, 58 with SiLU, 68 with bias and GELU;
 // with expf, a division per element and erff 82 and 105.
 
 __device__ __forceinline__ float exp2_approx(float x)          // 2^-22 relative, subnormal results 0
@@ -74,7 +74,7 @@ __device__ __forceinline__ f32x2 gelu_tanh_arg(f32x2 x)
 // reweighted least squares; of the p between 0.2 and 0.5 the best). So Q, and x Q in the negative tail
 // of GELU, is relatively exact, (2^-19 + z^2 2^-23) with the roundings, and no 1 - erf cancels. (An
 // absolute 1.5e-7 with five terms left 6e-4 of GELU(-4.2), more than half a step of fp16; 8192 x 6144 x
-// 2048 with bias and GELU took 66.0 us with it.)
+// 2048 with bias and GELU took 64.3 us with it, 67.6 now.)
 __device__ __forceinline__ f32x2 normal_tails(f32x2 x, f32x2& z, f32x2& e)
 {
     constexpr float kHalfLog2e = 0.72134752044448170f, kP = 0.305f;

@@ -1587,7 +1587,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constan
             bool ok = mbar_wait(&acc_full_bar[acc], acc_phase, ab, kErrEpiAccFull);
             // (the warps of a fused token-major tile share nothing, and with bias, activation and
             // residual each goes on by itself: 8192 x 6144 x 2048 with a residual 63.5 against 64.7 us, with
-            // bias and GELU 63.4 against 67. The gated products, which gain nothing, keep the barrier.)
+            // bias and GELU (then of five terms) 63.4 against 67. The gated products, which gain nothing, keep the barrier.)
             if (Cfg::EPI_ROWS && Cfg::EPI == kEpiLinear && args.splits == 1) ok = __all_sync(0xffffffffu, ok);
             else ok = named_bar_and(1, 32 * kEpilogueWarps, ok);
             if (!ok) {
