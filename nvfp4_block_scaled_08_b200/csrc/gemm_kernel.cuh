@@ -748,7 +748,7 @@ __device__ __forceinline__ float actq_quantize_t(const GemmArgs& a, uint8_t* sme
 {
     using Raw = typename InTraits<T>::Raw;
     constexpr int U = 4;                                       // loads in flight per thread
-    const T* x = static_cast<const T*>(a.act);
+    const T* x = behind_wait(static_cast<const T*>(a.act));
     const int M = a.M;
     const uint32_t per_row = static_cast<uint32_t>(kcnt) * 32u;
     const uint32_t nvec = static_cast<uint32_t>(M) * per_row;

@@ -615,6 +615,12 @@ __device__ __forceinline__ const T* behind_wait(const T* p)
     asm volatile("" : "+l"(p));
     return p;
 }
+__device__ __forceinline__ uint4 ld_behind(const void* p)      // 16 bytes through such a pointer
+{
+    uint4 v;
+    asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 
 // ... and allow the next grid in the stream, if launched with the attribute, to start.
 __device__ __forceinline__ void grid_launch_dependents()

@@ -15,6 +15,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "ptx.cuh"
+
 namespace nvfp4 {
 
 // fp32 -> e4m3fn byte, round to nearest even, finite values saturate to +-448.
@@ -82,7 +84,8 @@ __device__ __forceinline__ uint32_t scale_to_e2m1x8(const float (&v)[8], float r
 }
 
 // Every lane handles a "vector" of 8 consecutive elements (two lanes per 16-element block):
-// 32 bytes of fp32 (two 16-byte loads) or 16 bytes of bf16.
+// 32 bytes of fp32 (two 16-byte loads) or 16 bytes of bf16. Kernels that may start before the
+// one that writes the input has ended load through behind_wait(): not as constant data.
 struct Raw32 {
     uint4 lo, hi;
 };
@@ -93,7 +96,7 @@ template <> struct InTraits<float> {
     using Raw = Raw32;
     __device__ static Raw load(const float* p)
     {
-        return Raw32{__ldg(reinterpret_cast<const uint4*>(p)), __ldg(reinterpret_cast<const uint4*>(p + 4))};
+        return Raw32{ld_behind(p), ld_behind(p + 4)};
     }
     __device__ static Raw zero() { return Raw32{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}; }
     __device__ static void decode(const Raw& u, float (&v)[8])
@@ -107,7 +110,7 @@ template <> struct InTraits<float> {
 template <> struct InTraits<__nv_bfloat16> {
     static constexpr int kPerThread = 8;
     using Raw = uint4;
-    __device__ static Raw load(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ static Raw load(const __nv_bfloat16* p) { return ld_behind(p); }
     __device__ static Raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
     __device__ static void decode(const Raw& u, float (&v)[8])
     {

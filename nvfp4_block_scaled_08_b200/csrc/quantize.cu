@@ -105,14 +105,15 @@ __global__ void __launch_bounds__(THREADS) quantize_dynamic_kernel(
     const uint32_t nblocks = gridDim.x;
     const uint32_t bid = blockIdx.x;
     grid_dependency_wait();      // launched early behind the previous kernel: wait for its data
+    const GlobalVecs<T> in{behind_wait(x), ix};
 
     uint32_t v0 = 0, v1 = 0;
     float m;
     if constexpr (RESIDENT) {
         block_range(nv, chunk, bid, v0, v1);
-        m = amax_sweep<T>(GlobalVecs<T>{x, ix}, v0 + threadIdx.x, v1, blockDim.x, stash, v0);
+        m = amax_sweep<T>(in, v0 + threadIdx.x, v1, blockDim.x, stash, v0);
     } else {
-        m = amax_sweep<T>(GlobalVecs<T>{x, ix}, bid * blockDim.x + threadIdx.x, nv, nblocks * blockDim.x);
+        m = amax_sweep<T>(in, bid * blockDim.x + threadIdx.x, nv, nblocks * blockDim.x);
     }
     m = block_max(m, red);
     if (threadIdx.x == 0) {
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(THREADS) quantize_dynamic_kernel(
     if (bid == 0) {
         if (threadIdx.x == 0) *gs_out = gs;
         for (int32_t i = threadIdx.x; i < n_alpha; i += blockDim.x)
-            alpha_out[i] = __fdiv_rn(1.0f, __fmul_rn(gs, gs_other[i]));
+            alpha_out[i] = __fdiv_rn(1.0f, __fmul_rn(gs, ld_written(gs_other + i)));
     }
     // a dependent GEMM may start its prologue now (it waits for this grid before reading)
     cudaTriggerProgrammaticLaunchCompletion();
@@ -158,8 +159,8 @@ __global__ void __launch_bounds__(THREADS) quantize_dynamic_kernel(
     if constexpr (RESIDENT) {
         quantize_sweep<T>(StashVecs<T>{stash, v0}, v0 + (threadIdx.x & ~31u), v1, blockDim.x, gs, rcp_tab, dst);
     } else {
-        quantize_sweep<T>(GlobalVecs<T>{x, ix}, bid * blockDim.x + (threadIdx.x & ~31u), nv,
-                          nblocks * blockDim.x, gs, rcp_tab, dst, true);
+        quantize_sweep<T>(in, bid * blockDim.x + (threadIdx.x & ~31u), nv, nblocks * blockDim.x, gs, rcp_tab, dst,
+                          true);
     }
 }
 
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(512) quantize_dynamic_cluster_kernel(
     grid_dependency_wait();      // launched early behind the previous kernel: wait for its data
     uint32_t v0, v1;
     block_range(nv, chunk, blockIdx.y, v0, v1);
-    float m = amax_sweep<T>(GlobalVecs<T>{x, ix}, v0 + threadIdx.x, v1, blockDim.x, stash, v0);
+    float m = amax_sweep<T>(GlobalVecs<T>{behind_wait(x), ix}, v0 + threadIdx.x, v1, blockDim.x, stash, v0);
     m = block_max(m, red);
     if (threadIdx.x == 0) cta_max = m;
     cluster_sync();                                   // every CTA's maximum is in place
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(512) quantize_dynamic_cluster_kernel(
     if (blockIdx.y == 0) {
         if (threadIdx.x == 0) *gs_out = gs;
         for (int32_t i = threadIdx.x; i < n_alpha; i += blockDim.x)
-            alpha_out[i] = __fdiv_rn(1.0f, __fmul_rn(gs, gs_other[i]));
+            alpha_out[i] = __fdiv_rn(1.0f, __fmul_rn(gs, ld_written(gs_other + i)));
     }
     cudaTriggerProgrammaticLaunchCompletion();
     __shared__ float rcp_tab[256];
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(512) mx_quantize_kernel(const T* __restrict__ 
                                                           uint8_t* __restrict__ q, const SfOut sfo)
 {
     grid_dependency_wait();      // launched early behind the previous kernel: wait for its data
-    mx_quantize_sweep<T>(GlobalVecs<T>{x, ix}, blockIdx.x * blockDim.x + (threadIdx.x & ~31u), nv,
+    mx_quantize_sweep<T>(GlobalVecs<T>{behind_wait(x), ix}, blockIdx.x * blockDim.x + (threadIdx.x & ~31u), nv,
                          gridDim.x * blockDim.x, q, sfo);
 }
 

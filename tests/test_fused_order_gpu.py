@@ -79,3 +79,36 @@ def test_scalars_and_bias_written_just_before(cuda_device, M):
     want = run(True)
     for _ in range(5):
         assert all(torch.equal(g, w) for g, w in zip(run(False), want))
+
+
+@pytest.mark.parametrize("M,dtype", [(1, torch.bfloat16), (40, torch.float32), (3000, torch.bfloat16), (3000, torch.float32)], ids=str)
+def test_quantisers_behind_a_product(cuda_device, M, dtype):
+    """The quantisers, and the product that quantises its activations itself, directly behind the product that
+    writes their input (and another's global scale)."""
+    d, K = cuda_device, 1024
+    a, sa, ga, _ = quantised(workloads.normal(M, K, 1.0, 31).to(d))
+    b, sb, gb, _ = quantised(workloads.normal(K, K, 0.05, 32).to(d))
+    al = nv.alpha(ga, gb)
+
+    def run(idle):
+        wait = torch.cuda.synchronize if idle else (lambda: None)
+        x = torch.full((M, K), 1e9, dtype=dtype, device=d)
+        torch.cuda.synchronize()
+        out = []
+        nv.gemm_epilogue(a, sa, b, sb, al, out=x, act="silu")
+        wait()
+        out += nv.quantize_dynamic(x, gs_other=gb, tiled=False)
+        nv.gemm_epilogue(a, sa, b, sb, al, out=x, act="relu")
+        wait()
+        out += nv.mx_quantize(x, tiled=False)
+        if M <= 64:
+            nv.gemm_epilogue(a, sa, b, sb, al, out=x, act="gelu")
+            wait()
+            out.append(nv.gemm_act(x, gb, b, sb))
+        torch.cuda.synchronize()
+        return [o for r in out for o in (r if isinstance(r, tuple) else (r,))]
+
+    want = run(True)
+    for _ in range(5):
+        got = run(False)
+        assert len(got) == len(want) and all(torch.equal(g, w) for g, w in zip(got, want))

@@ -56,3 +56,17 @@ def test_every_split_k_launch_drains_its_receive_barrier():
     guards = re.findall(r"if constexpr \(([^;]*?)\) \{", text[:at])
     assert guards[-1] == "!Cfg::GROUPED && !Cfg::PAIR"
     assert text.rindex("if (warp == 4 && lane == 0 && args.splits > 1 && args.cluster_size > 1)", 0, at) > text.rindex(guards[-1], 0, at)
+
+
+def test_quantisers_load_behind_the_wait():
+    """The same of the quantisers that may start early: their input is loaded through behind_wait()."""
+    core = code("quant_core.cuh")
+    load = core[core.index("template <> struct InTraits<float>"):core.index("struct GlobalVecs")]
+    assert "__ldg" not in load and load.count("ld_behind(p") == 3
+    text = code("quantize.cu")
+    for kernel in text.split("__global__")[1:]:
+        if "grid_dependency_wait();" in kernel:
+            body = kernel[kernel.index("grid_dependency_wait();"):]
+            assert set(re.findall(r"GlobalVecs<T>(?: in)?\{([^,]*),", kernel)) == {"behind_wait(x)"}
+            assert "behind_wait(x)" in body and "gs_other[" not in body and "__ldg" not in body
+    assert "behind_wait(static_cast<const T*>(a.act))" in code("gemm_kernel.cuh")
