@@ -48,9 +48,11 @@ def test_vectors_written_just_before(cuda_device, T, H):
             assert all(torch.equal(g, w) for g, w in zip(run(False, scale), want))
 
 
-@pytest.mark.parametrize("M", [1, 64, 300])
-def test_scalars_and_bias_written_just_before(cuda_device, M):
-    """alpha, gs_h and the bias come from kernels launched just before the products that read them."""
+@pytest.mark.parametrize("b_ready", [False, True])
+@pytest.mark.parametrize("M", [1, 64, 300, 2500])
+def test_scalars_and_bias_written_just_before(cuda_device, M, b_ready):
+    """alpha, gs_h, the bias, the residual and dh come from kernels launched just before the products that read
+    them (b_ready is about the weights alone, which stay as they are)."""
     d, H, I = cuda_device, 1024, 512
     x = workloads.normal(M, H, 1.0, 21).to(d)
     w = workloads.normal(2 * I, H, 0.05, 22).to(d)
@@ -66,15 +68,19 @@ def test_scalars_and_bias_written_just_before(cuda_device, M):
         torch.cuda.synchronize()
         nv.gemm_epilogue(a, sa, b, sb, first, out=vec)
         wait()
-        lin = nv.gemm_epilogue(a, sa, b, sb, first, bias=vec[M - 1], act="gelu")
+        lin = nv.gemm_epilogue(a, sa, b, sb, first, bias=vec[M - 1], act="gelu", b_ready=b_ready)
+        wait()
+        res = nv.gemm_epilogue(a, sa, b, sb, first, residual=lin, b_ready=b_ready)
         gs_h = nv.global_scale(wide)
         wait()
-        q, sf = nv.gemm_glu_quantize(a, sa, b, sg, first, gs_h, tiled=False)
+        q, sf = nv.gemm_glu_quantize(a, sa, b, sg, first, gs_h, tiled=False, b_ready=b_ready)
         al = nv.alpha(ga, gb)
         wait()
-        h = nv.gemm_glu(a, sa, b, sg, al)
+        h = nv.gemm_glu(a, sa, b, sg, al, b_ready=b_ready)
+        wait()
+        dgu = nv.gemm_glu_backward(a, sa, b, sg, al, h, b_ready=b_ready)
         torch.cuda.synchronize()
-        return lin, q, sf, h
+        return lin, res, q, sf, h, dgu
 
     want = run(True)
     for _ in range(5):
@@ -112,3 +118,39 @@ def test_quantisers_behind_a_product(cuda_device, M, dtype):
     for _ in range(5):
         got = run(False)
         assert len(got) == len(want) and all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_two_graphs_at_once(cuda_device):
+    """Two captured blocks replayed on two streams at once: no call shares memory with another."""
+    d, H, I = cuda_device, 1024, 512
+    jobs = []
+    for seed, M in ((41, 24), (42, 300)):
+        x, y = workloads.normal(M, H, 1.0, seed).to(d).bfloat16(), workloads.normal(M, H, 0.5, seed + 50).to(d).bfloat16()
+        w = 1 + workloads.normal(1, H, 0.1, seed + 100)[0].to(d)
+        b, _, gb, rows = quantised(workloads.normal(2 * I, H, 0.05, seed + 150).to(d))
+        sg = nv.gate_up_sf_tile(rows)
+        c, sc, gc, _ = quantised(workloads.normal(H, I, 0.05, seed + 200).to(d))
+        gn, gh = torch.full((1,), 300.0, device=d), torch.full((1,), 200.0, device=d)
+        al, al_c = nv.alpha(gn, gb), nv.alpha(gh, gc)
+
+        def block(x=x, y=y, w=w, b=b, sg=sg, c=c, sc=sc, gn=gn, gh=gh, al=al, al_c=al_c):
+            q, sf, r = nv.residual_norm_quantize(x, w, gn, y)
+            h, hs = nv.gemm_glu_quantize(q, sf, b, sg, al, gh, b_ready=True)
+            out = nv.gemm_epilogue(h, hs, c, sc, al_c, residual=r, b_ready=True)
+            return out, nv.gemm_glu_backward(q, sf, b, sg, al, torch.ones(x.shape[0], I, device=d, dtype=torch.bfloat16))
+
+        want = [o.clone() for o in block()]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = block()
+        jobs.append((g, got, want, torch.cuda.Stream(), block))      # (block holds the inputs)
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for g, _, _, s, _ in jobs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, got, want, _, _ in jobs:
+        assert all(torch.equal(o, w) for o, w in zip(got, want))
+    assert nv.last_device_error() == (0, 0)
